@@ -34,7 +34,8 @@ __all__ = ["delta_compress", "delta_decompress", "compress_batch", "decompress_b
            "CompressBatch", "DecompressBatch", "StreamedDecompress", "RemappedBatch",
            "decompress_remapped", "race_compress", "race_decompress", "codec_available",
            "RaceFrame", "DEFAULT_RACE", "FormatError", "ChecksumError",
-           "CapacityError", "max_payload_bytes", "workspace_bytes", "FORMAT"]
+           "CapacityError", "max_payload_bytes", "workspace_bytes", "FORMAT", "AdamWBatch",
+           "GradNormBatch"]
 
 
 class FormatError(ValueError):
@@ -657,3 +658,7 @@ def race_decompress(frames, threads: int = 0, pin: bool = False) -> list[torch.T
             err = FormatError if jobs[j].status == EFORMAT else RuntimeError
             raise err(f"frame {j}: {_native.status_string(jobs[j].status)}")
     return outs
+
+
+# the trainer's step that makes the new weights
+from .step import AdamWBatch, GradNormBatch  # noqa: E402

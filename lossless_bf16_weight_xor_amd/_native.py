@@ -29,6 +29,10 @@ EXPORTED = ("bf16d_max_payload_bytes", "bf16d_workspace_bytes",
             "bf16d_race_decompress", "bf16d_compress_bound", "bf16d_decompress_bound",
             "bf16d_decompress_noalloc", "bf16d_decompress_verified", "bf16d_remap_plan_bytes", "bf16d_remap_map_bytes",
             "bf16d_remap_prepare", "bf16d_decompress_remapped_prepared")
+# the optimizer step, declared in bf16delta_step.h
+STEP_EXPORTED = ("bf16d_grad_norm_table_bytes", "bf16d_grad_norm_prepare", "bf16d_grad_norm",
+                 "bf16d_adamw_table_bytes", "bf16d_adamw_prepare", "bf16d_adamw_step")
+GRAD_BF16, GRAD_F32 = 0, 1
 # the benchmark's measurement aids, in their own library (bf16delta_probe.h)
 PROBE_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbf16delta_probe.so")
 PROBE_EXPORTED = ("bf16d_probe_read", "bf16d_probe_inplace", "bf16d_probe_write")
@@ -89,6 +93,30 @@ class RaceJob(ctypes.Structure):
 
 class Events(ctypes.Structure):
     _fields_ = [("before", ctypes.c_void_p), ("after", ctypes.c_void_p)]
+
+
+class StepPlan(ctypes.Structure):
+    _fields_ = [("opaque", ctypes.c_uint64 * 8)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("n", ctypes.c_uint64), ("dtype", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class AdamWJob(ctypes.Structure):
+    _fields_ = [("weights", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_uint64),
+                ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("grad_dtype", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_uint64), ("seed", ctypes.c_uint64),
+                ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p)]
 
 
 RESULT_BYTES = ctypes.sizeof(Result)
@@ -178,6 +206,22 @@ def lib():
         L.bf16d_decompress_remapped_prepared.restype = ctypes.c_int
         L.bf16d_decompress_noalloc.argtypes = [ctypes.POINTER(DecompressJob), u32, vp, vp]
         L.bf16d_decompress_noalloc.restype = ctypes.c_int
+        L.bf16d_grad_norm_table_bytes.argtypes = [u64, u32]
+        L.bf16d_grad_norm_table_bytes.restype = sz
+        L.bf16d_grad_norm_prepare.argtypes = [ctypes.POINTER(Grad), u32, vp, sz, vp, vp,
+                                              ctypes.POINTER(StepPlan)]
+        L.bf16d_grad_norm_prepare.restype = ctypes.c_int
+        L.bf16d_grad_norm.argtypes = [ctypes.POINTER(StepPlan), ctypes.c_double, ctypes.c_double,
+                                      vp]
+        L.bf16d_grad_norm.restype = ctypes.c_int
+        L.bf16d_adamw_table_bytes.argtypes = [u64, u32]
+        L.bf16d_adamw_table_bytes.restype = sz
+        L.bf16d_adamw_prepare.argtypes = [ctypes.POINTER(AdamWJob), u32, u32, vp, sz, vp,
+                                          ctypes.POINTER(StepPlan)]
+        L.bf16d_adamw_prepare.restype = ctypes.c_int
+        L.bf16d_adamw_step.argtypes = [ctypes.POINTER(StepPlan), ctypes.POINTER(AdamWParams), vp,
+                                       vp]
+        L.bf16d_adamw_step.restype = ctypes.c_int
         _lib = L
     return _lib
 

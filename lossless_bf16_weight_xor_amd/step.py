@@ -1,0 +1,281 @@
+"""The trainer's side of a weight update (bf16delta_step.h): the AdamW step that
+makes a checkpoint's new BF16 weights, and the global gradient norm that
+clips it.  Argument marshalling only; the pair (old, new) goes on to
+CompressBatch.
+
+    norm = GradNormBatch(grads)
+    step = AdamWBatch(weights, grads, masters=masters, out=spare)
+    for t in range(1, steps + 1):
+        ...                                   # backward into grads
+        norm.run(max_norm=1.0)
+        step.run(lr=1e-5, step=t, norm=norm)  # spare holds the new weights
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Sequence
+
+import torch
+
+from . import _native
+from . import _check_rc, _stream, _weights_ptr
+
+_GRAD_TYPES = {torch.bfloat16: _native.GRAD_BF16, torch.float32: _native.GRAD_F32}
+_SPAN = 512          # elements: an arena's tensors start on multiples of this
+_SCALE_BLOCK = 32    # elements that share a scale byte
+
+
+def _device_ptr(t, what: str, dtypes, numel: int, device) -> int:
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{what} must be a tensor on a HIP device (got "
+                        f"{getattr(t, 'device', type(t))}); there is no CPU path")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be of type {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError("all tensors of a batch must be on one device")
+    if t.numel() != numel:
+        raise ValueError(f"{what} has {t.numel()} elements, {numel} are needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if numel and t.data_ptr() % 16:
+        raise ValueError(f"{what} must be 16-byte aligned")
+    return t.data_ptr() if numel else 0
+
+
+def _list(tensors, count: int, what: str) -> list:
+    tensors = list(tensors)
+    if len(tensors) != count:
+        raise ValueError(f"{what}: one tensor per weight tensor ({count}), got {len(tensors)}")
+    return tensors
+
+
+def _per_tensor(value, count: int, what: str) -> list:
+    values = [float(value)] * count if isinstance(value, (int, float)) else \
+        [float(x) for x in value]
+    if len(values) != count or not all(math.isfinite(x) and x >= 0.0 for x in values):
+        raise ValueError(f"{what} must be a finite number of at least 0, or one per tensor")
+    return values
+
+
+def _scalar_ptr(t: torch.Tensor, what: str, dtypes, device) -> int:
+    if t.dtype not in dtypes or t.device != device or t.numel() != 1:
+        raise TypeError(f"{what} must be a number or one {' or '.join(map(str, dtypes))} on the "
+                        f"batch's device")
+    return t.data_ptr()
+
+
+class _Prepared:
+    """A table uploaded once and a plan; calls on the current stream of its device."""
+
+    def _prepare(self, device: torch.device, table_bytes: int, call, what: str) -> None:
+        """call(table pointer, its bytes, stream, plan) -> status"""
+        self.device = device
+        with torch.cuda.device(device):
+            self.table = torch.empty(table_bytes, dtype=torch.uint8, device=device)
+            self.plan = _native.StepPlan()
+            self._stream0 = _stream(device)
+            _check_rc(call(self.table.data_ptr(), table_bytes, self._stream0,
+                           ctypes.byref(self.plan)), what)
+        self._plan_ref = ctypes.byref(self.plan)
+
+    def _owned(self) -> list:
+        """The buffers this object allocated."""
+        return [self.table]
+
+    def _call(self, fn, what: str, *args) -> None:
+        """fn(plan, *args, stream) on the current stream of the batch's device."""
+        stream = _stream(self.device)
+        if stream != self._stream0 and not torch.cuda.is_current_stream_capturing():
+            # the allocator may not reuse the buffers while this stream works on them
+            s = torch.cuda.current_stream(self.device)
+            for t in self._owned():
+                t.record_stream(s)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(self._plan_ref, *args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(self._plan_ref, *args, stream)
+        _check_rc(rc, what)
+
+
+class GradNormBatch(_Prepared):
+    """The global L2 norm of a fixed list of gradient tensors (bf16 or fp32,
+    mixed as they come), prepared once (bf16d_grad_norm).
+
+    run() enqueues one kernel on the current stream; it may be captured into
+    a graph (keep this object and the gradients alive as long as the graph).
+    The outcome stays on the device, as 0-dim views of one small buffer:
+      norm      : float64, |grad_scale| * sqrt(sum of squares)
+      scale     : float32, grad_scale * min(1, max_norm / norm), what
+                  AdamWBatch multiplies the gradients by
+      nonfinite : int32, 1 if a gradient is infinite or NaN (AdamWBatch then
+                  leaves the step out)
+    The gradients' addresses are fixed: zero them in place between steps.  Calls of
+    one object must not overlap in time."""
+
+    def __init__(self, grads: Sequence[torch.Tensor]):
+        self.grads = list(grads)   # keep the tensors alive
+        if not self.grads:
+            raise ValueError("empty batch")
+        count = len(self.grads)
+        device = getattr(self.grads[0], "device", None)
+        jobs = (_native.Grad * count)()
+        for j, g in enumerate(self.grads):
+            n = g.numel() if isinstance(g, torch.Tensor) else 0
+            p = _device_ptr(g, "gradient", tuple(_GRAD_TYPES), n, device)
+            jobs[j] = _native.Grad(p, n, _GRAD_TYPES[g.dtype], 0)
+        self.result = torch.zeros(2, dtype=torch.float64, device=device)
+        self.norm = self.result[0]
+        words = self.result.view(torch.int32)
+        self.scale = words[2:3].view(torch.float32)[0]
+        self.nonfinite = words[3]
+        lib = _native.lib()
+        self._fn = lib.bf16d_grad_norm
+        total = sum(g.numel() for g in self.grads)
+        self._prepare(device, int(lib.bf16d_grad_norm_table_bytes(total, count)),
+                      lambda table, size, stream, plan: lib.bf16d_grad_norm_prepare(
+                          jobs, count, table, size, self.result.data_ptr(), stream, plan),
+                      "bf16d_grad_norm_prepare")
+
+    def _owned(self) -> list:
+        return [self.table, self.result]
+
+    def run(self, max_norm: float = math.inf, grad_scale: float = 1.0) -> None:
+        """max_norm: above 0, infinity for no clipping.  grad_scale: what the
+        stored gradients are multiplied by (finite)."""
+        if not max_norm > 0 or not math.isfinite(grad_scale):
+            raise ValueError("max_norm must be above 0 and grad_scale finite")
+        self._call(self._fn, "bf16d_grad_norm", max_norm, grad_scale)
+
+
+class AdamWBatch(_Prepared):
+    """One AdamW step over a fixed list of tensors, prepared once
+    (bf16d_adamw_step; the formulas, the rounding and the 8-bit states are
+    described in bf16delta_step.h).
+
+    weights : bf16 tensors, the working weights before the step
+    grads   : bf16 or fp32, one per weight tensor
+    masters : fp32 master copies, updated in place; without them the bf16
+              weights are what is trained, and are rounded stochastically
+    out     : bf16 tensors that receive the new weights; None for in place.
+              With two working copies, the batch (a -> b) and another one
+              (b -> a) over the same states take turns, and pairs() is what
+              CompressBatch takes.
+    states  : (m, v) lists of fp32 tensors, or for state_bits=8 (m, v,
+              m_scale, v_scale): uint8 (or float8_e4m3fn) codes, and uint8 (or
+              float8_e8m0fnu) scale bytes, one per 32 elements.  They are
+              updated in place.  None: zeros, allocated here (the attributes
+              m, v, m_scale, v_scale are the lists in either case).
+    weight_decay, lr_scale : a number, or one per tensor
+    A tensor that several names share is listed once.  All buffers keep their
+    addresses.  Calls of one object must not overlap in time."""
+
+    def __init__(self, weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+                 masters: Sequence[torch.Tensor] | None = None,
+                 out: Sequence[torch.Tensor] | None = None, states=None, state_bits: int = 32,
+                 weight_decay=0.01, lr_scale=1.0):
+        self.weights = list(weights)
+        if not self.weights:
+            raise ValueError("empty batch")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        count = len(self.weights)
+        self.state_bits = state_bits
+        self.grads = _list(grads, count, "grads")
+        self.masters = None if masters is None else _list(masters, count, "masters")
+        self.out = self.weights if out is None else _list(out, count, "out")
+        for w in self.weights:
+            _weights_ptr(w, "weights")
+            if w.dtype != torch.bfloat16:
+                raise TypeError(f"weights must be bfloat16, got {w.dtype}")
+        device = self.weights[0].device
+        sizes = [w.numel() for w in self.weights]
+        parts = 2 if state_bits == 32 else 4
+        if states is None:
+            states = self._new_states(sizes, device)
+        elif len(states) != parts:
+            raise ValueError(f"states must be {parts} lists of tensors for {state_bits}-bit states")
+        names = ("m", "v", "m_scale", "v_scale")[:parts]
+        lists = [_list(s, count, name) for s, name in zip(states, names)]
+        self.m, self.v = lists[:2]
+        self.m_scale, self.v_scale = lists[2:] if parts == 4 else (None, None)
+        decay = _per_tensor(weight_decay, count, "weight_decay")
+        rate = _per_tensor(lr_scale, count, "lr_scale")
+        code = (torch.float32,) if state_bits == 32 else (torch.uint8, torch.float8_e4m3fn)
+        byte = (torch.uint8, torch.float8_e8m0fnu)
+        jobs = (_native.AdamWJob * count)()
+        for j, n in enumerate(sizes):
+            blocks = -(-n // _SCALE_BLOCK)
+            g = self.grads[j]
+            jobs[j] = _native.AdamWJob(
+                _device_ptr(self.weights[j], "weights", (torch.bfloat16,), n, device),
+                _device_ptr(self.out[j], "out", (torch.bfloat16,), n, device),
+                0 if masters is None else
+                _device_ptr(self.masters[j], "master", (torch.float32,), n, device),
+                _device_ptr(g, "gradient", tuple(_GRAD_TYPES), n, device),
+                _device_ptr(self.m[j], "m", code, n, device),
+                _device_ptr(self.v[j], "v", code, n, device),
+                0 if parts == 2 else _device_ptr(self.m_scale[j], "m_scale", byte, blocks, device),
+                0 if parts == 2 else _device_ptr(self.v_scale[j], "v_scale", byte, blocks, device),
+                n, rate[j], decay[j], _GRAD_TYPES[g.dtype], 0)
+        lib = _native.lib()
+        self._fn = lib.bf16d_adamw_step
+        self._params = _native.AdamWParams()
+        self._params_ref = ctypes.byref(self._params)
+        self._prepare(device, int(lib.bf16d_adamw_table_bytes(sum(sizes), count)),
+                      lambda table, size, stream, plan: lib.bf16d_adamw_prepare(
+                          jobs, count, state_bits, table, size, stream, plan),
+                      "bf16d_adamw_prepare")
+
+    def _new_states(self, sizes, device):
+        """Zero states of every tensor, as views of one arena per kind."""
+        starts, at = [], 0
+        for n in sizes:
+            starts.append(at)
+            at += -(-n // _SPAN) * _SPAN
+
+        def arena(dtype, per):
+            flat = torch.zeros(max(at, _SPAN) // per, dtype=dtype, device=device)
+            return [flat[a // per:a // per + -(-n // per)] for a, n in zip(starts, sizes)]
+
+        if self.state_bits == 32:
+            return arena(torch.float32, 1), arena(torch.float32, 1)
+        return (arena(torch.uint8, 1), arena(torch.uint8, 1), arena(torch.uint8, _SCALE_BLOCK),
+                arena(torch.uint8, _SCALE_BLOCK))
+
+    def pairs(self) -> list[tuple[torch.Tensor, torch.Tensor]]:
+        """(weights, out) per tensor, for CompressBatch; needs an `out` of its own."""
+        if self.out is self.weights:
+            raise ValueError("the step is done in place: there is no old copy to compare with")
+        return list(zip(self.weights, self.out))
+
+    def run(self, lr, step, betas: tuple[float, float] = (0.9, 0.95), eps: float = 1e-8,
+            seed: int = 0, norm: GradNormBatch | None = None) -> None:
+        """Enqueue one step on the current stream; it may be captured into a graph.
+
+        lr   : a number, or a float32 device tensor that the kernel reads
+        step : the step's number from 1, or an int64 device tensor that the
+               kernel reads (for graphs: advance it in the graph)
+        seed : of the stochastic rounding, with the step's number
+        norm : a GradNormBatch that has run on these gradients: its scale
+               multiplies them, and the step is left out if it found them not finite"""
+        p = self._params
+        p.lr_device = p.step_device = None
+        if isinstance(lr, torch.Tensor):
+            p.lr, p.lr_device = 0.0, _scalar_ptr(lr, "lr", (torch.float32,), self.device)
+        else:
+            p.lr = lr
+        if isinstance(step, torch.Tensor):
+            p.step, p.step_device = 1, _scalar_ptr(step, "step", (torch.int64,), self.device)
+        else:
+            p.step = step if step > 0 else 0
+        p.beta1, p.beta2 = betas
+        p.eps = eps
+        p.seed = seed & 0xFFFFFFFFFFFFFFFF
+        where = None
+        if norm is not None:
+            if norm.device != self.device:
+                raise ValueError("the norm and the step must be on one device")
+            where = norm.result.data_ptr()
+        self._call(self._fn, "bf16d_adamw_step", self._params_ref, where)
