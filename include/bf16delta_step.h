@@ -112,8 +112,8 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
  *
  * 8-bit states: element i stands for e4m3(code[i]) * 2^(scale[i / 32] - 127),
  * e4m3 being the 4-exponent 3-mantissa-bit float (largest value 448, no
- * infinities, 0x7F NaN) and the scale byte an 8-bit exponent (a byte of 0,
- * as in freshly cleared states, makes the block 0).  At each step a block's
+ * infinities, 0x7F and 0xFF NaN) and the scale byte an 8-bit exponent (255
+ * stands for nothing).  Cleared states (all bytes 0) are zeros.  At each step a block's
  * scale is the smallest power of two, at least 2^-126, with which its largest
  * finite magnitude does not pass 448, and each magnitude is rounded stochastically
  * to the e4m3 grid.  A positive v is never rounded to 0 (the smallest code

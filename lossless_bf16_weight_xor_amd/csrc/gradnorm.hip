@@ -30,13 +30,12 @@ __device__ __forceinline__ void add_word(double (&s)[2], const u32x4 &w) {
 
 template <bool kF32>
 __device__ __forceinline__ void add_chunk(double (&s)[2], BF16D_GMEM const void *grad,
-                                          uint64_t first, uint64_t n) {
+                                          uint64_t first, bool full, uint32_t count) {
     constexpr uint32_t kPer = kF32 ? 4 : 8;                       // elements of a word
     constexpr uint32_t kWords = kNormChunk / kPer / kThreads;     // words of a thread
     BF16D_GMEM const uint8_t *p =
         (BF16D_GMEM const uint8_t *)grad + first * (kF32 ? 4 : 2);
-    const uint64_t left = n - first;
-    if (left >= kNormChunk) {
+    if (full) {
         u32x4 w[kWords];
 #pragma unroll
         for (uint32_t k = 0; k < kWords; ++k)
@@ -45,12 +44,12 @@ __device__ __forceinline__ void add_chunk(double (&s)[2], BF16D_GMEM const void 
         for (uint32_t k = 0; k < kWords; ++k) add_word<kF32>(s, w[k]);
         return;
     }
-    const uint32_t words = (uint32_t)left / kPer;
+    const uint32_t words = count / kPer;
     for (uint32_t k = threadIdx.x; k < words; k += kThreads)
         add_word<kF32>(s, *((BF16D_GMEM const u32x4 *)p + k));
     // the last word's elements, one a thread
     const uint32_t i = words * kPer + threadIdx.x;
-    if (threadIdx.x < kPer && i < (uint32_t)left) {
+    if (threadIdx.x < kPer && i < count) {
         if constexpr (kF32) add_square(s[0], ((BF16D_GMEM const uint32_t *)p)[i]);
         else add_square(s[0], (uint32_t)((BF16D_GMEM const uint16_t *)p)[i] << 16);
     }
@@ -71,11 +70,13 @@ __device__ __forceinline__ double group_sum(double v, double *s_tmp) {
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormArgs a) {
     __shared__ double s_tmp[kWaves];
     double s[2] = {0.0, 0.0};
-    for (uint64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-        const NormJob &J = a.jobs[a.map[c]];
-        const uint64_t first = (c - J.chunk0) * kNormChunk;
-        if (J.dtype == BF16D_GRAD_F32) add_chunk<true>(s, J.grad, first, J.n);
-        else add_chunk<false>(s, J.grad, first, J.n);
+    for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        const NormJob J = a.jobs[a.map[c]];
+        const uint32_t chunk = c - J.chunk0;   // of the tensor
+        const uint64_t first = (uint64_t)chunk * kNormChunk;
+        const bool full = chunk < J.full_chunks;
+        if (J.dtype == BF16D_GRAD_F32) add_chunk<true>(s, J.grad, first, full, J.tail);
+        else add_chunk<false>(s, J.grad, first, full, J.tail);
     }
     const double mine = group_sum(s[0] + s[1], s_tmp);
     // the partial sum is handed over by a returning device-scope atomic, as

@@ -21,7 +21,7 @@ struct Plan {
     bf16d_norm_result *result;
     int32_t device;
     uint32_t state_bits;
-    uint64_t reserved;
+    uint32_t lds_bytes, reserved;
 };
 static_assert(sizeof(Plan) == sizeof(bf16d_step_plan), "the plan is opaque words");
 constexpr uint64_t kNormMagic = 0x4D524F4E44363146ull;    // "F16DNORM"
@@ -112,8 +112,9 @@ int norm_prepare(const bf16d_grad *grads, uint32_t count, void *table, size_t ta
     uint64_t c = 0;
     for (uint32_t j = 0; j < count; ++j) {
         dj[j].grad = (BF16D_GMEM const void *)grads[j].grad;
-        dj[j].n = grads[j].n;
-        dj[j].chunk0 = c;
+        dj[j].chunk0 = uint32_t(c);
+        dj[j].full_chunks = uint32_t(grads[j].n / kNormChunk);
+        dj[j].tail = uint32_t(grads[j].n % kNormChunk);
         dj[j].dtype = grads[j].dtype;
         for (const uint64_t end = c + chunks_of(grads[j].n, kNormChunk); c < end; ++c) map[c] = j;
     }
@@ -129,6 +130,15 @@ int norm_prepare(const bf16d_grad *grads, uint32_t count, void *table, size_t ta
     return up;
 }
 
+// The LDS a workgroup (one wave) of the step asks for, to limit how many run on
+// a CU at once: kAdamFlight bytes of loads in flight, by the batch's mean.
+uint32_t flight_lds(uint64_t loaded, uint64_t total) {
+    if (total == 0) return 0;
+    const double wave = double(loaded) / double(total) * kAdamGroup;   // bytes a wave loads
+    const double waves = kAdamFlight / wave;
+    return waves >= 31.0 ? 0 : uint32_t(kLdsBytes / waves) & ~1023u;
+}
+
 bool rate_ok(float x) { return std::isfinite(x) && x >= 0.0f; }
 
 int adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bits, void *table,
@@ -139,7 +149,7 @@ int adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bi
     const bool bits8 = state_bits == 8;
     std::vector<Range> ranges;
     ranges.reserve(8 * size_t(count) + 1);
-    uint64_t chunks = 0, number = 0;
+    uint64_t chunks = 0, number = 0, total = 0, loaded = 0;
     for (uint32_t j = 0; j < count; ++j) {
         const bf16d_adamw_job &J = jobs[j];
         if (J.n > kMaxSize / 4 || J.grad_dtype > BF16D_GRAD_F32 || J.reserved != 0 ||
@@ -157,6 +167,9 @@ int adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bi
         }
         chunks += chunks_of(J.n, kAdamChunk);
         if (chunks >= kMaxTiles) return BF16D_EINVAL;
+        total += J.n;
+        loaded += J.n * ((J.master ? 4 : 2) + (J.grad_dtype == BF16D_GRAD_F32 ? 4 : 2) +
+                         (bits8 ? 2 : 8));
         const uint64_t state = bits8 ? J.n : 4 * J.n;
         const uint64_t scales = bits8 ? chunks_of(J.n, kScaleBlock) : 0;
         // without a master copy the weights may be updated in place: each
@@ -192,11 +205,12 @@ int adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bi
         dj[j].v = (BF16D_GMEM void *)J.v;
         dj[j].m_scale = (BF16D_GMEM uint8_t *)J.m_scale;
         dj[j].v_scale = (BF16D_GMEM uint8_t *)J.v_scale;
-        dj[j].n = J.n;
-        dj[j].chunk0 = c;
         dj[j].number0 = number;
+        dj[j].chunk0 = uint32_t(c);
+        dj[j].full_chunks = uint32_t(J.n / kAdamChunk);
+        dj[j].tail = uint32_t(J.n % kAdamChunk);
         dj[j].lr_scale = J.lr_scale;
-        dj[j].weight_decay = J.weight_decay;
+        dj[j].decay = J.lr_scale * J.weight_decay;
         dj[j].grad_dtype = J.grad_dtype;
         number += align_up(J.n, kNumberSpan);
         for (const uint64_t end = c + chunks_of(J.n, kAdamChunk); c < end; ++c) map[c] = j;
@@ -207,6 +221,7 @@ int adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bi
     p.map = reinterpret_cast<const uint32_t *>(base + t.map);
     p.chunks = chunks;
     p.state_bits = state_bits;
+    p.lds_bytes = flight_lds(loaded, total);
     const int up = upload(table, host, stream);
     if (up == BF16D_OK) std::memcpy(plan, &p, sizeof p);
     return up;
@@ -266,7 +281,7 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
     a.partial = static_cast<uint64_t *>(p.partial);
     a.done = reinterpret_cast<uint32_t *>(a.partial + kNormGrid);
     a.result = p.result;
-    a.chunks = p.chunks;
+    a.chunks = uint32_t(p.chunks);
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
     launch_grad_norm(a, stream);
@@ -310,8 +325,7 @@ int bf16d_adamw_step(const bf16d_step_plan *plan, const bf16d_adamw_params *para
     // beta 0 has logarithm -infinity, and 1 - beta^t = -expm1(-infinity) = 1
     a.log_beta1 = std::log(P.beta1);
     a.log_beta2 = std::log(P.beta2);
-    a.c1 = -std::expm1(double(P.step) * a.log_beta1);
-    a.c2 = -std::expm1(double(P.step) * a.log_beta2);
+    a.numbers = step_numbers(P.lr, P.step, P.seed, a.log_beta1, a.log_beta2);
     a.beta1 = float(P.beta1);
     a.beta2 = float(P.beta2);
     a.rest1 = float(1.0 - P.beta1);
@@ -319,7 +333,8 @@ int bf16d_adamw_step(const bf16d_step_plan *plan, const bf16d_adamw_params *para
     a.eps = float(P.eps);
     a.seed = P.seed;
     a.step = P.step;
-    launch_adamw(a, uint32_t(p.chunks), p.state_bits, stream);
+    a.groups = uint32_t(p.chunks) * kAdamSplit;
+    launch_adamw(a, p.state_bits, p.lds_bytes, stream);
     return hipGetLastError() == hipSuccess ? BF16D_OK : BF16D_EHIP;
 }
 

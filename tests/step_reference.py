@@ -6,13 +6,17 @@ Bounds.  u = 2^-24 is half a step of fp32.  Every 32-bit operation, and every
 constant rounded to 32 bits, adds at most u of its result:
   m   = beta1 m0 + rest1 g : 3u on the first term (constant, product, sum),
         4u on the second (constant, g = scale * grad, product, sum)
-  v   = beta2 v0 + rest2 g g : 3u, and 6u (constant, g twice, two products, sum)
-  d   = sqrt(v) root2 + eps : 3u from v, u each for root, root2, product, sum
-        and eps, at most 8u of d
-  upd = rate m / d : the bound of m carried through, and u each for rate, product
-        and quotient beside d's 8u: 11u
-  p   = p0 - (decay p0 + upd) : 3u of decay p0 (constant, product, sum), u of upd
-        for the sum, u of p for the difference
+  v   = beta2 v0 + rest2 g g : 3u, and 6u (constant, g twice, two products, sum);
+        both terms are positive
+  d   = sqrt(v) root2 + eps : 3u from v (6u halved), 2u for the root (good to
+        one unit in the last place), u each for root2, product, sum and eps, and u
+        for a denormal v taken for 0: at most 11u of d
+  upd = rate (m (1 / d)) : the bound of m carried through, 2u for the reciprocal, 2u
+        for rate (lr / c1 and its product with lr_scale) and u each for the two
+        products, beside d's 11u
+  p   = p0 - (decay p0 + upd) : 5u of decay p0 (lr, lr_scale * weight_decay, their
+        product, its product with p0, sum), u of upd for the sum, u of p for
+        the difference
 and 1 % on top for the products of bounds.  What is rounded to fewer bits after
 that is compared through the rounding itself, which is monotone: it has to lie
 between the roundings of value - bound and value + bound.
@@ -64,8 +68,8 @@ E4M3 = e4m3_values()
 
 
 def decode(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
-    """The values that 8-bit states stand for (a scale byte of 0: zeros)."""
-    s = np.where(scale == 0, 0.0, 2.0 ** (scale.astype(np.float64) - 127))
+    """The values that 8-bit states stand for."""
+    s = 2.0 ** (scale.astype(np.float64) - 127)
     return E4M3[codes] * np.repeat(s, 32)[:codes.size]
 
 
@@ -147,9 +151,9 @@ class Tensor:
         upd = lr * (self.m / c1) / d
         self.p = p0 - lr * decay * p0 - upd
         # sqrt(v) where v is itself only known to a few of the smallest fp32 steps
-        d_off = 8 * U + np.sqrt(TINY / c2) / d
-        self.p_off = 1.01 * (lr / c1 / d * self.m_off + np.abs(upd) * (4 * U + d_off)
-                             + U * (3 * lr * decay * np.abs(p0) + np.abs(self.p))) + TINY
+        d_off = 11 * U + np.sqrt(TINY / c2) / d
+        self.p_off = 1.01 * (lr / c1 / d * self.m_off + np.abs(upd) * (6 * U + d_off)
+                             + U * (5 * lr * decay * np.abs(p0) + np.abs(self.p))) + TINY
 
 
 def check_f32(got: np.ndarray, want: np.ndarray, off: np.ndarray, what: str) -> None:

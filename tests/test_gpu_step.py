@@ -150,6 +150,38 @@ def test_step_over_its_parameters(bits, betas, eps, step):
     m.check(m.before, step=step, decay=[0.2] * 3, lr_scale=rates, **kw)
 
 
+@pytest.mark.parametrize("master", [True, False], ids=["master", "no master"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_nothing_around_the_tensors_is_written(bits, master):
+    """Every array is a view into one buffer, with 16 to 31 guard bytes before and
+    behind it: the guards keep their pattern, in a step, in one that is left
+    out, and with the norm in between."""
+    log(f"guards bits={bits} master={master}")
+    m = Model(SIZES, 91, bits, master, apart=True)
+    lists = [m.out, m.grads, *m.states] + ([m.masters] if master else [m.weights])
+    total = sum(x.numel() * x.element_size() + 64 for part in lists for x in part)
+    buffer = torch.full((total,), 0xA5, dtype=torch.uint8, device=DEV)
+    inside = torch.zeros(total, dtype=torch.bool, device=DEV)
+    at = 16
+    for part in lists:
+        for j, x in enumerate(part):
+            size = x.numel() * x.element_size()
+            view = buffer[at:at + size].view(x.dtype)
+            view.copy_(x)
+            part[j] = view
+            inside[at:at + size] = True
+            at += -(-size // 16) * 16 + 16
+    norm, batch = GradNormBatch(m.grads), m.batch(weight_decay=0.1)
+    norm.run(1.0)
+    batch.run(lr=1e-3, step=1, norm=norm)
+    m.grads[-1][0] = math.nan
+    norm.run(1.0)
+    batch.run(lr=1e-3, step=2, norm=norm)
+    torch.cuda.synchronize()
+    assert norm.nonfinite.item() == 1
+    assert bool((buffer[~inside] == 0xA5).all())
+
+
 def test_a_fresh_state_starts_from_zeros():
     for bits in (32, 8):
         log(f"fresh states bits={bits}")
