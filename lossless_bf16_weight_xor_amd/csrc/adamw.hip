@@ -48,16 +48,23 @@ struct Scalars {
     uint32_t key0, key1;
 };
 
-// 32 random bits for each of the elements numbered e .. e + 3, e a multiple of
-// 4.  The four differ in the two lowest bits only, so the first shifted word
-// is the same for all.
-__device__ __forceinline__ void random_bits(uint32_t (&r)[4], uint64_t e, const Scalars &s) {
-    const uint32_t x = (uint32_t)e ^ s.key0;
-    const uint32_t y = x ^ (x >> 16);
-    const uint32_t add = s.key1 + (uint32_t)(e >> 32) * 0x9E3779B9u;
+// 32 random bits for each of the lane's four elements, numbered
+// first + 4 * lane + q.  first is a multiple of 256 and the same in the whole wave,
+// so are then the bits of a number from the 8th on, and with them the shifted
+// word of the first mixing step; what q adds to its product is a scalar, too.
+__device__ __forceinline__ void random_bits(uint32_t (&r)[4], uint64_t first, const Scalars &s) {
+    static_assert(kAdamGroup == 256 && kNumberSpan % 256 == 0 && kAdamChunk % 256 == 0,
+                  "a workgroup's first number is a multiple of 256");
+    constexpr uint32_t kMul = 0xBF58476Du;
+    const uint32_t x = (uint32_t)first ^ s.key0;
+    const uint32_t y = x ^ (x >> 16);   // of element 0; element i has y ^ i
+    const uint32_t add = s.key1 + (uint32_t)(first >> 32) * 0x9E3779B9u;
+    const uint32_t product = (y ^ (4 * threadIdx.x)) * kMul;
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-        uint32_t z = (y ^ q) * 0xBF58476Du + add;
+        // kept apart by first_lane: the compiler would multiply for each element
+        const uint32_t more = first_lane(add + (((y ^ q) & 3) - (y & 3)) * kMul);
+        uint32_t z = product + more;
         z = (z ^ (z >> 15)) * 0x94D049BBu;
         r[q] = z ^ (z >> 16);
     }
@@ -191,19 +198,18 @@ __device__ __forceinline__ uint32_t to_codes(const f32x4 &x, const uint32_t (&r)
 // takes part.  v has no signs (NaN aside); one above 0 gets at least code 1.
 __device__ __forceinline__ void encode(const f32x4 &m, const f32x4 &v, const uint32_t (&random)[4],
                                        uint32_t &mc, uint32_t &vc, uint32_t &mb, uint32_t &vb) {
-    uint32_t am[4], av[4], r[4];
+    uint32_t av[4], r[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        am[k] = __float_as_uint(m[k]) & 0x7FFFFFFFu;
-        av[k] = __float_as_uint(v[k]);
-    }
-    uint32_t mt = block_max(umax32(umax32(am[0], am[1]), umax32(am[2], am[3])));
+    for (int k = 0; k < 4; ++k) av[k] = __float_as_uint(v[k]);
+    // the largest |m| leaves NaN out by itself; as bits, for v, NaN is the largest
+    uint32_t mt = block_max(__float_as_uint(
+        fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3])))));
     uint32_t vt = block_max(umax32(umax32(av[0], av[1]), umax32(av[2], av[3])));
     if (__ballot(umax32(mt, vt) >= kInfBits)) {   // wave-uniform, rare: leave them out
         mt = vt = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            mt = umax32(mt, finite_bits(am[k]));
+            mt = umax32(mt, finite_bits(__float_as_uint(m[k]) & 0x7FFFFFFFu));
             vt = umax32(vt, finite_bits(av[k]));
         }
         mt = block_max(mt);
@@ -260,7 +266,7 @@ __device__ __forceinline__ void step_four(const Group &c, const Scalars &s) {
         v = load_f32<kFull>((BF16D_GMEM const float *)c.v + i, valid);
     }
     uint32_t random[4];
-    if constexpr (kBits == 8 || !kMaster) random_bits(random, c.number + i, s);
+    if constexpr (kBits == 8 || !kMaster) random_bits(random, c.number, s);
     if constexpr (!kF32) g = widen(gh);
     if constexpr (!kMaster) p = widen(ph);
     if constexpr (kBits == 8) {
@@ -332,19 +338,6 @@ __device__ __forceinline__ void copy_group(const AdamJob &J, uint64_t first, uin
     const u32x2 w = J.master ? nearest_bf16(load_f32<false>(J.master + at, valid))
                              : load_16<false>(J.weights + at, valid);
     store_16<false>(J.out + at, w, valid);
-}
-
-// The table does not change while kernels run, so its entries are read as
-// constants (scalar loads, though the kernel stores through other pointers).
-template <typename T>
-__device__ __forceinline__ T load_constant(const T *p) {
-    struct Words {
-        uint32_t w[sizeof(T) / 4];
-    } x;
-    auto *q = (const __attribute__((address_space(4))) uint32_t *)(uintptr_t)p;
-#pragma unroll
-    for (uint32_t k = 0; k < sizeof(T) / 4; ++k) x.w[k] = q[k];
-    return __builtin_bit_cast(T, x);
 }
 
 template <int kBits, bool kExact>
