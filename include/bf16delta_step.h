@@ -153,8 +153,9 @@ typedef struct bf16d_adamw_job {
     uint32_t        reserved;       /* 0 */
 } bf16d_adamw_job;
 
-/* lr: finite, not negative; beta1, beta2: in [0, 1); eps: at least 2^-126 and
- * finite; step: from 1.  lr_device (4-byte aligned) and step_device (8-byte
+/* lr: finite, not negative; beta1, beta2: in [0, 1); eps: from 2^-50 (8.9e-16;
+ * beside a smaller one, the root of a v too small for fp32 would count) to
+ * 2^100; step: from 1.  lr_device (4-byte aligned) and step_device (8-byte
  * aligned), where not NULL, are device words read by the kernel in place of
  * lr and step, for calls captured in a graph; a step word of 0 counts as 1. */
 typedef struct bf16d_adamw_params {

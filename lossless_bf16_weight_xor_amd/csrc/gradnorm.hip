@@ -3,8 +3,9 @@
 //
 // norm = |c| sqrt(sum g^2).  One pass over the gradients, 2 or 4 bytes and
 // one 64-bit multiply-add an element: bound by the read (7.1 TB/s in bf16, 6.8
-// in fp32).  The loads are non-temporal, 8 % faster than plain ones, and the
-// next turn's table entry is fetched a turn ahead.
+// in fp32).  The loads are non-temporal, 8 % faster than plain ones in a large
+// batch, but for what the step that follows can find in the caches; the next
+// turn's table entry is fetched a turn ahead.
 #include "step.hpp"
 
 namespace bf16d {
@@ -30,7 +31,14 @@ __device__ __forceinline__ void add_word(double (&s)[2], const u32x4 &w) {
     }
 }
 
-template <bool kF32>
+template <bool kKeep>
+__device__ __forceinline__ u32x4 load_word(BF16D_GMEM const u32x4 *p) {
+    if constexpr (kKeep) return *p;
+    else return __builtin_nontemporal_load(p);
+}
+
+// kKeep: the words may stay in the caches
+template <bool kF32, bool kKeep>
 __device__ __forceinline__ void add_chunk(double (&s)[2], BF16D_GMEM const void *grad,
                                           uint64_t first, bool full, uint32_t count) {
     constexpr uint32_t kPer = kF32 ? 4 : 8;                       // elements of a word
@@ -41,8 +49,7 @@ __device__ __forceinline__ void add_chunk(double (&s)[2], BF16D_GMEM const void 
         u32x4 w[kWords];
 #pragma unroll
         for (uint32_t k = 0; k < kWords; ++k)
-            w[k] = __builtin_nontemporal_load((BF16D_GMEM const u32x4 *)p + k * kThreads +
-                                              threadIdx.x);
+            w[k] = load_word<kKeep>((BF16D_GMEM const u32x4 *)p + k * kThreads + threadIdx.x);
 #pragma unroll
         for (uint32_t k = 0; k < kWords; ++k) add_word<kF32>(s, w[k]);
         return;
@@ -70,20 +77,31 @@ __device__ __forceinline__ double group_sum(double v, double *s_tmp) {
     return t;
 }
 
+// kKept: the batch's first chunks are left in the caches (its own kernel: the
+// other one is 2 % slower with the choice in it)
+template <bool kKept>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormArgs a) {
     __shared__ double s_tmp[kWaves];
     double s[2] = {0.0, 0.0};
-    uint32_t c = blockIdx.x;
-    uint32_t j = c < a.chunks ? load_constant(a.map + c) : 0;
-    while (c < a.chunks) {
+    // turn t reads the t-th chunk, from the end where some are kept
+    auto chunk_of = [&](uint32_t t) { return kKept ? a.chunks - 1 - t : t; };
+    uint32_t t = blockIdx.x;
+    uint32_t j = t < a.chunks ? load_constant(a.map + chunk_of(t)) : 0;
+    while (t < a.chunks) {
         const NormJob J = load_constant(a.jobs + j);
+        const uint32_t c = chunk_of(t);
         const uint32_t chunk = c - J.chunk0;   // of the tensor
-        c += gridDim.x;
-        if (c < a.chunks) j = load_constant(a.map + c);
+        t += gridDim.x;
+        if (t < a.chunks) j = load_constant(a.map + chunk_of(t));
         const uint64_t first = (uint64_t)chunk * kNormChunk;
         const bool full = chunk < J.full_chunks;
-        if (J.dtype == BF16D_GRAD_F32) add_chunk<true>(s, J.grad, first, full, J.tail);
-        else add_chunk<false>(s, J.grad, first, full, J.tail);
+        if (J.dtype == BF16D_GRAD_F32) {
+            if (kKept && c < a.kept) add_chunk<true, true>(s, J.grad, first, full, J.tail);
+            else add_chunk<true, false>(s, J.grad, first, full, J.tail);
+        } else {
+            if (kKept && c < a.kept) add_chunk<false, true>(s, J.grad, first, full, J.tail);
+            else add_chunk<false, false>(s, J.grad, first, full, J.tail);
+        }
     }
     const double mine = group_sum(s[0] + s[1], s_tmp);
     // the partial sum is handed over by a returning device-scope atomic, as
@@ -94,10 +112,10 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormArgs a) {
                                     (uint64_t)__double_as_longlong(mine), __ATOMIC_RELAXED,
                                     __HIP_MEMORY_SCOPE_AGENT);
     if (!last_workgroup(a.done, dep)) return;
-    double t = 0.0;
+    double all = 0.0;
     for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads)
-        t += __longlong_as_double((long long)ld_relaxed_agent(a.partial + b));
-    const double sum = group_sum(t, s_tmp);
+        all += __longlong_as_double((long long)ld_relaxed_agent(a.partial + b));
+    const double sum = group_sum(all, s_tmp);
     if (threadIdx.x == 0) {
         const double norm = fabs(a.grad_scale) * sqrt(sum);
         a.result->norm = norm;
@@ -113,7 +131,8 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormArgs a) {
 void launch_grad_norm(const NormArgs &a, hipStream_t stream) {
     const uint32_t grid =
         (uint32_t)(a.chunks < kNormGrid ? (a.chunks ? a.chunks : 1) : kNormGrid);
-    grad_norm_kernel<<<grid, kThreads, 0, stream>>>(a);
+    auto *kernel = a.kept ? grad_norm_kernel<true> : grad_norm_kernel<false>;
+    kernel<<<grid, kThreads, 0, stream>>>(a);
 }
 
 }  // namespace bf16d

@@ -21,7 +21,7 @@ struct Plan {
     bf16d_norm_result *result;
     int32_t device;
     uint32_t state_bits;
-    uint32_t lds_bytes, reserved;
+    uint32_t lds_bytes, kept;
 };
 static_assert(sizeof(Plan) == sizeof(bf16d_step_plan), "the plan is opaque words");
 constexpr uint64_t kNormMagic = 0x4D524F4E44363146ull;    // "F16DNORM"
@@ -87,15 +87,21 @@ int norm_prepare(const bf16d_grad *grads, uint32_t count, void *table, size_t ta
         return BF16D_EINVAL;
     std::vector<Range> ranges;
     ranges.reserve(size_t(count) + 2);
-    uint64_t chunks = 0;
+    uint64_t chunks = 0, bytes = 0, kept = 0;
     for (uint32_t j = 0; j < count; ++j) {
         const bf16d_grad &G = grads[j];
         if (G.n > kMaxSize / 4 || G.dtype > BF16D_GRAD_F32 || G.reserved != 0 ||
             (G.n > 0 && (!G.grad || !aligned16(G.grad))))
             return BF16D_EINVAL;
+        const uint64_t size = G.dtype == BF16D_GRAD_F32 ? 4 : 2;
         chunks += chunks_of(G.n, kNormChunk);
         if (chunks >= kMaxTiles) return BF16D_EINVAL;
-        add_range(ranges, G.grad, G.n * (G.dtype == BF16D_GRAD_F32 ? 4 : 2), false);
+        // the chunks that begin within the first kNormKept bytes
+        if (bytes < kNormKept)
+            kept += std::min(chunks_of(G.n, kNormChunk),
+                             chunks_of(kNormKept - bytes, uint32_t(kNormChunk * size)));
+        bytes += G.n * size;
+        add_range(ranges, G.grad, G.n * size, false);
     }
     const Table t = table_layout(sizeof(NormJob), count, chunks, true);
     if (table_bytes < t.total) return BF16D_EINVAL;
@@ -125,6 +131,7 @@ int norm_prepare(const bf16d_grad *grads, uint32_t count, void *table, size_t ta
     p.chunks = chunks;
     p.partial = base + t.partial;
     p.result = result;
+    p.kept = bytes <= kNormKeptTotal ? uint32_t(kept) : 0;
     const int up = upload(table, host, stream);
     if (up == BF16D_OK) std::memcpy(plan, &p, sizeof p);
     return up;
@@ -282,6 +289,7 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
     a.done = reinterpret_cast<uint32_t *>(a.partial + kNormGrid);
     a.result = p.result;
     a.chunks = uint32_t(p.chunks);
+    a.kept = p.kept;
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
     launch_grad_norm(a, stream);
@@ -308,8 +316,9 @@ int bf16d_adamw_step(const bf16d_step_plan *plan, const bf16d_adamw_params *para
         (reinterpret_cast<uintptr_t>(params->step_device) & 7u) != 0)
         return BF16D_EINVAL;
     const bf16d_adamw_params &P = *params;
-    if (!beta_ok(P.beta1) || !beta_ok(P.beta2) || !std::isfinite(P.eps) ||
-        !(P.eps >= 1.1754943508222875e-38) || P.eps > 3.4e38)
+    // below 2^-50 the root of a v that fp32 cannot hold would count, and a 1 / d
+    // of a larger eps than 2^100 would be denormal
+    if (!beta_ok(P.beta1) || !beta_ok(P.beta2) || !(P.eps >= 0x1p-50) || !(P.eps <= 0x1p100))
         return BF16D_EINVAL;
     if (!P.lr_device && !(std::isfinite(P.lr) && P.lr >= 0.0)) return BF16D_EINVAL;
     if (!P.step_device && P.step == 0) return BF16D_EINVAL;

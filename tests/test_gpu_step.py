@@ -198,14 +198,65 @@ def test_a_fresh_state_starts_from_zeros():
         m.check(before, step=1, decay=[0.0] * 4, **kw)
 
 
-def test_elements_around_two_to_the_32_have_numbers_of_their_own():
-    """Element numbers are 64 bits wide: two jobs whose numbers agree in the low
-    32 bits are rounded differently.  (Checked through many small jobs' numbers
-    only, as a job that long would not fit a test: the kernel's numbers are
-    those of the reference, which holds them in 64 bits.)"""
-    a = ref.random_bits(0, 64, 1, 1)
-    b = ref.random_bits(1 << 32, 64, 1, 1)
-    assert (a != b).all()
+def test_a_tensor_of_more_than_two_to_the_33_elements():
+    """Offsets beyond 32 bits, element numbers that use the high word, and more
+    workgroups than one launch holds: slices around 2^32, around the launch's
+    2^33 elements and at the end, the rest zeros."""
+    log("2^33 elements")
+    n = (1 << 33) + 4096 + 77
+    zeros = lambda dtype, k=n: torch.zeros(k, dtype=dtype, device=DEV)
+    w, g = zeros(torch.bfloat16), zeros(torch.bfloat16)
+    states = (zeros(torch.uint8), zeros(torch.uint8), zeros(torch.uint8, -(-n // 32)),
+              zeros(torch.uint8, -(-n // 32)))
+    slices = [((1 << 32) - 1024, 2048), ((1 << 33) - 512, n - (1 << 33) + 512), (0, 256)]
+    gen = _gen(17)
+    for a, k in slices:
+        w[a:a + k] = _normal(k, gen, 0.02).to(torch.bfloat16)
+        g[a:a + k] = _normal(k, gen, 1e-3).to(torch.bfloat16)
+    before = [(to_u16(w[a:a + k]), _np(g[a:a + k])) for a, k in slices]
+    kw = dict(lr=1e-3, betas=(0.9, 0.95), eps=1e-8)
+    norm = GradNormBatch([g])
+    norm.run()
+    AdamWBatch([w], [g], states=[[x] for x in states], state_bits=8, weight_decay=0.1).run(
+        step=3, seed=6, norm=norm, **kw)
+    torch.cuda.synchronize()
+    assert norm.norm.item() == pytest.approx(math.sqrt(sum(float((x ** 2).sum())
+                                                           for _, x in before)), rel=1e-12)
+    for (a, k), (bits, grad) in zip(slices, before):
+        t = ref.Tensor(ref.bf16_values(bits), grad, np.zeros(k), np.zeros(k), lr=1e-3, beta1=0.9,
+                       beta2=0.95, eps=1e-8, decay=0.1, t=3)
+        r = ref.random_bits(a, k, 6, 3)
+        ref.check_weights(to_u16(w[a:a + k]), t, (r * np.uint32(0x9E3779B1)) >> np.uint32(16),
+                          f"weights from {a}")
+        m, v, ms, vs = (x[a // per:-(-(a + k) // per)].cpu().numpy()
+                        for x, per in zip(states, (1, 1, 32, 32)))
+        ref.check_state8(m, ms, t.m, t.m_off, r & np.uint32(0xFFFF), False, f"m from {a}")
+        ref.check_state8(v, vs, t.v, t.v_off, r >> np.uint32(16), True, f"v from {a}")
+    assert not states[0][(1 << 32) + 1024:(1 << 32) + (1 << 20)].any()
+
+
+def test_denormal_second_moments_beside_a_small_eps():
+    """v below the smallest normal fp32 number still has its root where eps does
+    not hide it (the exact root's variant): without it the updates would be 1e-4
+    off.  Beside a far smaller eps, v itself may be lost: refused."""
+    log("denormal v")
+    for bits in (32, 8):
+        m = Model([4096, 33], 5, bits, True, grads="fp32", spread=False)
+        for j, g in enumerate(m.grads):
+            g.mul_(1e-16)                      # g around 1e-19, v around 1e-39
+            m.masters[j].zero_()
+            for part in m.states:
+                part[j].zero_()
+        before = m.snapshot()
+        kw = dict(lr=1e-3, betas=(0.9, 0.9), eps=1e-15)
+        batch = m.batch(weight_decay=0.0)
+        batch.run(step=1, **kw)
+        torch.cuda.synchronize()
+        m.check(before, step=1, decay=[0.0, 0.0], **kw)
+        for g in m.grads:
+            g.mul_(10.0)
+        with pytest.raises(RuntimeError, match="EINVAL"):
+            batch.run(lr=1e-3, step=1, betas=(0.9, 0.9), eps=1e-30)
 
 
 def test_eight_bit_states_on_extreme_values():
@@ -341,6 +392,22 @@ def test_norm_matches_its_definition(sizes):
         assert norm.nonfinite.item() == 0
     a = norm.result.clone()
     norm.run(1e-20, 3.0)
+    assert torch.equal(a.view(torch.int64), norm.result.view(torch.int64))
+
+
+def test_norm_of_a_batch_beyond_the_caches():
+    """More than 1 GiB of gradients: read from the first chunk on, nothing kept."""
+    log("norm of 1.3 GiB")
+    gen = _gen(3)
+    grads = [_normal(n, gen, 1e-3).to(torch.bfloat16) for n in (400_000_003, 300_000_001, 77)]
+    want = math.sqrt(sum(float(x.double().square().sum()) for g in grads
+                         for x in g.split(1 << 26)))
+    norm = GradNormBatch(grads)
+    norm.run(1.0)
+    a = norm.result.clone()
+    norm.run(1.0)
+    torch.cuda.synchronize()
+    assert abs(norm.norm.item() - want) <= 1e-7 * 2.0 ** -10 * want
     assert torch.equal(a.view(torch.int64), norm.result.view(torch.int64))
 
 

@@ -179,7 +179,7 @@ def test_run_calls_refuse_foreign_plans_and_bad_numbers(native):
     for name in ("beta1", "beta2"):
         for x in (-0.1, 1.0, 1.5, NAN):
             assert call(**{name: x}) == E
-    for eps in (0.0, -1e-8, 1e-39, NAN, INF, 1e39):
+    for eps in (0.0, -1e-8, 1e-39, 1e-30, 8.8e-16, NAN, INF, 1e39, 2.0 ** 101):
         assert call(eps=eps) == E
     for lr in (-1e-3, NAN, INF):
         assert call(lr=lr) == E
