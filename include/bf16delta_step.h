@@ -147,13 +147,13 @@ typedef struct bf16d_adamw_job {
     uint8_t        *m_scale;
     uint8_t        *v_scale;
     uint64_t        n;
-    float           lr_scale;       /* finite, not negative */
-    float           weight_decay;   /* finite, not negative */
+    float           lr_scale;       /* these two and their product: */
+    float           weight_decay;   /*   finite, not negative */
     uint32_t        grad_dtype;     /* BF16D_GRAD_* */
     uint32_t        reserved;       /* 0 */
 } bf16d_adamw_job;
 
-/* lr: finite, not negative; beta1, beta2: in [0, 1); eps: from 2^-50 (8.9e-16;
+/* lr: finite in fp32, not negative; beta1, beta2: in [0, 1); eps: from 2^-50 (8.9e-16;
  * beside a smaller one, the root of a v too small for fp32 would count) to
  * 2^100; step: from 1.  lr_device (4-byte aligned) and step_device (8-byte
  * aligned), where not NULL, are device words read by the kernel in place of

@@ -160,7 +160,8 @@ int adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bi
     for (uint32_t j = 0; j < count; ++j) {
         const bf16d_adamw_job &J = jobs[j];
         if (J.n > kMaxSize / 4 || J.grad_dtype > BF16D_GRAD_F32 || J.reserved != 0 ||
-            !rate_ok(J.lr_scale) || !rate_ok(J.weight_decay))
+            !rate_ok(J.lr_scale) || !rate_ok(J.weight_decay) ||
+            !rate_ok(J.lr_scale * J.weight_decay))
             return BF16D_EINVAL;
         if (!aligned16(J.weights) || !aligned16(J.out) || !aligned16(J.master) ||
             !aligned16(J.grad) || !aligned16(J.m) || !aligned16(J.v) || !aligned16(J.m_scale) ||
@@ -320,7 +321,7 @@ int bf16d_adamw_step(const bf16d_step_plan *plan, const bf16d_adamw_params *para
     // of a larger eps than 2^100 would be denormal
     if (!beta_ok(P.beta1) || !beta_ok(P.beta2) || !(P.eps >= 0x1p-50) || !(P.eps <= 0x1p100))
         return BF16D_EINVAL;
-    if (!P.lr_device && !(std::isfinite(P.lr) && P.lr >= 0.0)) return BF16D_EINVAL;
+    if (!P.lr_device && !rate_ok(float(P.lr))) return BF16D_EINVAL;
     if (!P.step_device && P.step == 0) return BF16D_EINVAL;
     rc = check_device(p, stream);
     if (rc != BF16D_OK) return rc;

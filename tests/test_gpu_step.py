@@ -546,6 +546,76 @@ def test_captured_steps_are_those_run_eagerly(bits, master):
         assert torch.equal(norms[0].result, norms[1].result)
 
 
+@pytest.mark.parametrize("betas,step", [((0.0, 0.0), 1), ((0.9, 0.999), 1), ((0.9, 0.95), 0),
+                                        ((0.99, 0.9999), 12345678901)])
+def test_rate_and_step_number_from_the_device(betas, step):
+    """The kernel's own bias corrections; a step word of 0 counts as 1."""
+    log(f"device numbers betas={betas} step={step}")
+    sizes = [4097, 33, 0, 1000]
+    for bits in (32, 8):
+        for lr_there, step_there in ((True, True), (True, False), (False, True)):
+            if step == 0 and not step_there:
+                continue
+            m = Model(sizes, 7, bits, False)
+            kw = dict(betas=betas, eps=1e-8, seed=12)
+            m.batch(weight_decay=0.3).run(
+                lr=torch.tensor(0.25, device=DEV) if lr_there else 0.25,
+                step=torch.tensor([step], device=DEV) if step_there else step, **kw)
+            torch.cuda.synchronize()
+            m.check(m.before, lr=0.25, step=max(step, 1), decay=[0.3] * 4, **kw)
+
+
+def test_device_numbers_of_another_kind_are_refused():
+    log("device numbers refused")
+    m = Model([64], 7, 32, True)
+    batch = m.batch()
+    for lr in (torch.tensor(1.0), torch.ones(2, device=DEV),
+               torch.tensor(1.0, dtype=torch.float64, device=DEV)):
+        with pytest.raises(TypeError):
+            batch.run(lr=lr, step=1)
+    for step in (torch.tensor(1), torch.tensor(1, dtype=torch.int32, device=DEV)):
+        with pytest.raises(TypeError):
+            batch.run(lr=1.0, step=step)
+    for step in (0, -1):
+        with pytest.raises(RuntimeError, match="EINVAL"):
+            batch.run(lr=1.0, step=step)
+
+
+def test_lists_that_do_not_fit_are_refused():
+    log("lists refused")
+    m = Model([64, 40], 7, 8, True)
+    good = dict(masters=m.masters, states=m.states, state_bits=8)
+    cut = [m.grads[0], m.grads[1][:39]]
+    for change, error in (
+            (dict(masters=[x.half() for x in m.masters]), TypeError),
+            (dict(masters=[x.cpu() for x in m.masters]), TypeError),
+            (dict(masters=m.masters[::-1]), ValueError),
+            (dict(out=[torch.empty(128, dtype=torch.bfloat16, device=DEV)[::2], m.weights[1]]),
+             ValueError),
+            (dict(out=[torch.empty(65, dtype=torch.bfloat16, device=DEV)[1:], m.weights[1]]),
+             ValueError),
+            (dict(states=m.states[:2]), ValueError),
+            (dict(states=(m.states[0], m.states[1], m.states[2], m.states[2][:1])), ValueError),
+            (dict(state_bits=32), ValueError),
+            (dict(weight_decay=[0.1]), ValueError),
+            (dict(weight_decay=-0.1), ValueError),
+            (dict(lr_scale=math.nan), ValueError)):
+        with pytest.raises(error):
+            AdamWBatch(m.weights, m.grads, **{**good, **change})
+    with pytest.raises(ValueError):
+        AdamWBatch(m.weights, cut, **good)
+    with pytest.raises(TypeError):
+        GradNormBatch([m.grads[0].half()])
+    with pytest.raises(ValueError):
+        m.batch().pairs()
+    norm = GradNormBatch(m.grads)
+    for bad in (0.0, -1.0, math.nan):
+        with pytest.raises(ValueError):
+            norm.run(bad)
+    with pytest.raises(ValueError):
+        norm.run(1.0, math.inf)
+
+
 def test_runs_on_another_stream():
     log("another stream")
     a, b = (Model(SIZES, 71, 8, True) for _ in range(2))

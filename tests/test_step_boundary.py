@@ -112,6 +112,7 @@ def test_adamw_prepare_refusals(native):
     for name in ("lr_scale", "weight_decay"):
         for x in (NAN, INF, -1.0):
             assert call(**{name: x}) == E, (name, x)
+    assert call(lr_scale=1e30, weight_decay=1e30) == E
     assert call(grad_dtype=2) == E and call(reserved=1) == E
     for n in ((1 << 62) + 1, 1 << 62, (1 << 64) - 1, 1 << 50):
         assert call(n=n) == E
@@ -181,7 +182,7 @@ def test_run_calls_refuse_foreign_plans_and_bad_numbers(native):
             assert call(**{name: x}) == E
     for eps in (0.0, -1e-8, 1e-39, 1e-30, 8.8e-16, NAN, INF, 1e39, 2.0 ** 101):
         assert call(eps=eps) == E
-    for lr in (-1e-3, NAN, INF):
+    for lr in (-1e-3, NAN, INF, 1e39):
         assert call(lr=lr) == E
     assert call(step=0) == E
     assert call(norm=BASE + 4) == E
