@@ -14,6 +14,9 @@ cross-region RL", section "Using ARCv3":
     restored = delta_decompress(src, payload, checksum)   # src is rebuilt in place
 
 The wire format is this project's own "bf16delta_v1", not ARCv3's.
+
+On the trainer's side, AdamWBatch and GradNormBatch (bf16delta_step.h) make the
+new weights that are compressed.
 """
 from __future__ import annotations
 
