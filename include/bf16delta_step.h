@@ -20,7 +20,8 @@
  * The table and every buffer of the jobs must stay valid, at the same
  * addresses, for as long as calls (or graphs that hold them) use the plan.
  * Calls that share a plan, a table or a written buffer must not overlap in
- * time.  BF16D_EHIP also reports a failed host allocation.
+ * time; nor must replays of graphs that hold such calls.  A batch holds fewer
+ * than 2^24 chunks of 4096 elements (6.8e10 elements).  BF16D_EHIP also reports a failed host allocation.
  */
 #ifndef BF16DELTA_STEP_H
 #define BF16DELTA_STEP_H
@@ -105,18 +106,18 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
  * share is one job).
  *
  * Rounding of the weights: with a master copy to the nearest, ties to even.
- * Without one stochastically (the next bf16 value away from zero is taken with the
- * probability that the value's position between the two says, in steps of
+ * Without one stochastically (the next bf16 value away from zero is taken with
+ * the probability that the value's position between the two says, in steps of
  * 2^-16): most updates of a step are far smaller than half a bf16 step, and
  * rounding to the nearest would lose them all.
  *
  * 8-bit states: element i stands for e4m3(code[i]) * 2^(scale[i / 32] - 127),
  * e4m3 being the 4-exponent 3-mantissa-bit float (largest value 448, no
  * infinities, 0x7F and 0xFF NaN) and the scale byte an 8-bit exponent (255
- * stands for nothing).  Cleared states (all bytes 0) are zeros.  At each step a block's
- * scale is the smallest power of two, at least 2^-126, with which its largest
- * finite magnitude does not pass 448, and each magnitude is rounded stochastically
- * to the e4m3 grid.  A positive v is never rounded to 0 (the smallest code
+ * stands for nothing).  Cleared states (all bytes 0) are zeros.  At each step a
+ * block's scale is the smallest power of two, at least 2^-126, with which its
+ * largest finite magnitude does not pass 448, and each magnitude is rounded
+ * stochastically to the e4m3 grid.  A positive v is never rounded to 0 (the smallest code
  * stands for it): m may not be divided by eps alone because v was lost.
  * Infinities and NaN are held as NaN, in their element only.
  * The rounding is stochastic because a step changes v by at most 1 - beta2 of

@@ -4,9 +4,12 @@
 //
 // One pass, nothing is read twice: a lane holds four consecutive elements of
 // every array, so each access of a wave is one contiguous run (1 KiB of an
-// fp32 array, 512 bytes of a bf16 one, 256 of a code array).  About 25
-// operations on 32-bit states and 60 on 8-bit ones against 28 and 16 bytes
-// an element: bound by HBM.
+// fp32 array, 512 bytes of a bf16 one, 256 of a code array).  With master
+// copies and bf16 gradients 17 vector instructions an element against 28 bytes
+// (32-bit states), or 37 against 16 (8-bit ones): bound by HBM, at 6.6 and
+// 6.3 TB/s for a 7B-shaped layer of 2.0e8 elements (854 and 519 us).  Without
+// master copies 8-bit states leave 10 bytes for 40 instructions: 6.4 TB/s, with
+// 83 % of the vector issue slots taken.
 //
 // 8-bit states: a block of 32 elements is 8 neighbouring lanes, so its
 // largest magnitude is three DPP steps inside a row of lanes, and no LDS is
@@ -15,7 +18,7 @@
 // converts both ways with the scale, and rounds stochastically to e4m3 and
 // bf16, in one instruction an element.  Written out in integer instructions
 // (with correctly rounded root and quotient, and no separate path for full
-// groups) the 8-bit step of a 7B-shaped layer took 859 us, now 525.
+// groups) the 8-bit step of that layer took 859 us.
 #include "step.hpp"
 
 namespace bf16d {
@@ -49,8 +52,8 @@ struct Scalars {
 };
 
 // 32 random bits for each of the lane's four elements, numbered
-// first + 4 * lane + q.  first is a multiple of 256 and the same in the whole wave,
-// so are then the bits of a number from the 8th on, and with them the shifted
+// first + 4 * lane + q.  first is a multiple of 256 and the same in the whole
+// wave, so the bits of a number from the 8th on are, and with them the shifted
 // word of the first mixing step; what q adds to its product is a scalar, too.
 __device__ __forceinline__ void random_bits(uint32_t (&r)[4], uint64_t first, const Scalars &s) {
     static_assert(kAdamGroup == 256 && kNumberSpan % 256 == 0 && kAdamChunk % 256 == 0,
@@ -170,8 +173,8 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// The scale byte of a block whose largest finite magnitude has the bits `top`: the
-// smallest b >= 1 with max |x| <= 448 * 2^(b - 127).  448 is 1.75 * 2^8, so b is
+// The scale byte of a block whose largest finite magnitude has the bits `top`:
+// the smallest b >= 1 with max |x| <= 448 * 2^(b - 127).  448 is 1.75 * 2^8, so b is
 // the exponent field less 8, and one more where the mantissa field passes
 // that of 1.75 (0x600000): a carry of the sum.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
@@ -194,8 +197,9 @@ __device__ __forceinline__ uint32_t to_codes(const f32x4 &x, const uint32_t (&r)
     return (uint32_t)c;
 }
 
-// Four of each moment to codes and the blocks' scale bytes.  Every lane of the wave
-// takes part.  v has no signs (NaN aside); one above 0 gets at least code 1.
+// Four of each moment to codes and the blocks' scale bytes.  Every lane of the
+// wave takes part.  v has no signs (NaN aside); one above 0 gets at least
+// code 1.
 __device__ __forceinline__ void encode(const f32x4 &m, const f32x4 &v, const uint32_t (&random)[4],
                                        uint32_t &mc, uint32_t &vc, uint32_t &mb, uint32_t &vb) {
     uint32_t av[4], r[4];

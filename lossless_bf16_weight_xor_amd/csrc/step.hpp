@@ -21,11 +21,11 @@ constexpr uint32_t kNormChunk = 4096;
 constexpr uint32_t kNormGrid = 1024;
 // In batches up to kNormKeptTotal the chunks are read from the last one back to
 // the first, and the first kNormKept bytes (the last-level cache's size) with
-// loads that leave them in the caches, where the step that follows begins.  Norm and step together, with
-// and without: 6e7 bf16 gradients 276 and 291 us with 32-bit states, 179 and
-// 191 with 8-bit ones; 2e8 fp32 ones 686 and 699.  Larger batches keep
-// too little of them, and are read faster from the first chunk on without
-// (1.6 GB in bf16: 1577 and 1600 us with 8-bit states).
+// loads that leave them in the caches, where the step that follows begins.
+// Norm and step together, with and without: 6e7 bf16 gradients 276 and 291 us
+// with 32-bit states, 179 and 191 with 8-bit ones; 2e8 fp32 ones 686 and 699.
+// Larger batches keep too little of them, and are read faster from the first
+// chunk on without (1.6 GB in bf16, 8-bit states: 1577 us, with 1600).
 constexpr uint64_t kNormKept = 256u << 20;
 constexpr uint64_t kNormKeptTotal = 1u << 30;
 

@@ -175,7 +175,9 @@ class AdamWBatch(_Prepared):
               m, v, m_scale, v_scale are the lists in either case).
     weight_decay, lr_scale : a number, or one per tensor
     A tensor that several names share is listed once.  All buffers keep their
-    addresses.  Calls of one object must not overlap in time."""
+    addresses: zero the gradients in place.  Calls of one object must not overlap
+    in time, nor replays of graphs that hold them (keep it alive as long as
+    those)."""
 
     def __init__(self, weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  masters: Sequence[torch.Tensor] | None = None,
@@ -262,7 +264,8 @@ class AdamWBatch(_Prepared):
 
         lr   : a number, or a float32 device tensor that the kernel reads
         step : the step's number from 1, or an int64 device tensor that the
-               kernel reads (for graphs: advance it in the graph)
+               kernel reads (for graphs: advance it in the graph, and keep
+               both tensors alive as long as it)
         seed : of the stochastic rounding, with the step's number
         norm : a GradNormBatch that has run on these gradients: its scale
                multiplies them, and the step is left out if it found them not finite"""

@@ -365,6 +365,29 @@ def test_non_finite_gradients_poison_their_element_only(bits, master):
             assert not np.isfinite(held).any()
 
 
+def test_a_lost_first_moment_stays_in_its_element():
+    """A NaN code in m alone: its block keeps the scale of the others."""
+    log("NaN in m")
+    n = 320
+    a, b = (Model([n], 22, 8, True, grads="fp32") for _ in range(2))
+    for x, code in ((a, 0), (b, 0xFF)):
+        x.grads[0][70] = 0.0
+        x.states[0][0][70] = code
+    for x in (a, b):
+        x.batch().run(lr=1e-3, step=3)
+    torch.cuda.synchronize()
+    x, y = a.snapshot(), b.snapshot()
+    keep = np.arange(n) != 70
+    for k in range(4):
+        if k < 2:
+            assert np.array_equal(x["s"][k][0][keep], y["s"][k][0][keep])
+        else:
+            assert np.array_equal(x["s"][k][0], y["s"][k][0])
+    assert np.array_equal(x["p"][0][keep], y["p"][0][keep])
+    assert np.isnan(y["p"][0][70]) and np.isnan(ref.E4M3[y["s"][0][0][70]])
+    assert x["s"][1][0][70] == y["s"][1][0][70]
+
+
 # ------------------------------------------------------------------- norm ---
 
 def _norm_of(grads, c=1.0):
@@ -544,6 +567,31 @@ def test_captured_steps_are_those_run_eagerly(bits, master):
         for i, j in zip(x["s"], y["s"]):
             assert all(np.array_equal(k, l) for k, l in zip(i, j)), t
         assert torch.equal(norms[0].result, norms[1].result)
+
+
+def test_two_graphs_of_one_batch_take_turns():
+    """Graphs that share a batch, its norm and their workspace, replayed in turn
+    with eager calls of the same batch in between."""
+    log("two graphs")
+    sizes = [20011, 333]
+    a, b = (Model(sizes, 62, 8, True) for _ in range(2))
+    (na, ba), (nb, bb) = ((GradNormBatch(x.grads), x.batch()) for x in (a, b))
+    one = lambda norm, batch, t: (norm.run(max_norm=0.5), batch.run(lr=1e-3, step=t, norm=norm))
+    graphs = []
+    for t in (3, 4):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            one(na, ba, t)
+        graphs.append(g)
+    for t in (3, 4, 5, 4, 3, 3, 4, 5):
+        graphs[t - 3].replay() if t < 5 else one(na, ba, t)
+        one(nb, bb, t)
+        torch.cuda.synchronize()
+        x, y = a.snapshot(), b.snapshot()
+        assert all(np.array_equal(i, j) for i, j in zip(x["out"], y["out"])), t
+        assert all(np.array_equal(k, l) for i, j in zip(x["s"], y["s"]) for k, l in zip(i, j)), t
+        assert torch.equal(na.result, nb.result)
 
 
 @pytest.mark.parametrize("betas,step", [((0.0, 0.0), 1), ((0.9, 0.999), 1), ((0.9, 0.95), 0),
