@@ -19,7 +19,7 @@ from typing import Sequence
 import torch
 
 from . import _native
-from . import _check_rc, _weights_ptr
+from . import _check_rc
 
 _GRAD_TYPES = {torch.bfloat16: _native.GRAD_BF16, torch.float32: _native.GRAD_F32}
 _SPAN = 512          # elements: an arena's tensors start on multiples of this
@@ -27,6 +27,16 @@ _SCALE_BLOCK = 32    # elements that share a scale byte
 
 
 def _device_ptr(t, what: str, dtypes, numel: int, device) -> int:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index
+            and t.dtype in dtypes and t.numel() == numel and t.is_contiguous()):
+        p = t.data_ptr()
+        if p % 16 == 0:
+            return p if numel else 0
+    _refuse(t, what, dtypes, numel, device)
+
+
+def _refuse(t, what: str, dtypes, numel: int, device) -> None:
+    """Says what is wrong with a tensor that _device_ptr did not take."""
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise TypeError(f"{what} must be a tensor on a HIP device (got "
                         f"{getattr(t, 'device', type(t))}); there is no CPU path")
@@ -38,9 +48,7 @@ def _device_ptr(t, what: str, dtypes, numel: int, device) -> int:
         raise ValueError(f"{what} has {t.numel()} elements, {numel} are needed")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if numel and t.data_ptr() % 16:
-        raise ValueError(f"{what} must be 16-byte aligned")
-    return t.data_ptr() if numel else 0
+    raise ValueError(f"{what} must be 16-byte aligned")
 
 
 def _list(tensors, count: int, what: str) -> list:
@@ -193,12 +201,10 @@ class AdamWBatch(_Prepared):
         self.grads = _list(grads, count, "grads")
         self.masters = None if masters is None else _list(masters, count, "masters")
         self.out = self.weights if out is None else _list(out, count, "out")
-        for w in self.weights:
-            _weights_ptr(w, "weights")
-            if w.dtype != torch.bfloat16:
-                raise TypeError(f"weights must be bfloat16, got {w.dtype}")
-        device = self.weights[0].device
-        sizes = [w.numel() for w in self.weights]
+        device = getattr(self.weights[0], "device", None)
+        sizes = [w.numel() if isinstance(w, torch.Tensor) else 0 for w in self.weights]
+        places = [_device_ptr(w, "weights", (torch.bfloat16,), n, device)
+                  for w, n in zip(self.weights, sizes)]
         parts = 2 if state_bits == 32 else 4
         if states is None:
             states = self._new_states(sizes, device)
@@ -217,7 +223,8 @@ class AdamWBatch(_Prepared):
             blocks = -(-n // _SCALE_BLOCK)
             g = self.grads[j]
             jobs[j] = _native.AdamWJob(
-                _device_ptr(self.weights[j], "weights", (torch.bfloat16,), n, device),
+                places[j],
+                places[j] if self.out is self.weights else
                 _device_ptr(self.out[j], "out", (torch.bfloat16,), n, device),
                 0 if masters is None else
                 _device_ptr(self.masters[j], "master", (torch.float32,), n, device),
