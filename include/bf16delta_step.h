@@ -117,12 +117,13 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
  * stands for nothing).  Cleared states (all bytes 0) are zeros.  At each step a
  * block's scale is the smallest power of two, at least 2^-126, with which its
  * largest finite magnitude does not pass 448, and each magnitude is rounded
- * stochastically to the e4m3 grid.  A positive v is never rounded to 0 (the smallest code
- * stands for it): m may not be divided by eps alone because v was lost.
+ * stochastically to the e4m3 grid.  A positive v is never rounded to 0 (the
+ * smallest code stands for it): m may not be divided by eps alone because v
+ * was lost.
  * Infinities and NaN are held as NaN, in their element only.
- * The rounding is stochastic because a step changes v by at most 1 - beta2 of
- * itself, less than half a step of the e4m3 grid: rounded to the nearest, v
- * would keep its first value.  Its price is noise without bias: against
+ * The rounding is stochastic because a step lowers v by at most 1 - beta2 of
+ * itself, at beta2 = 0.999 far less than half a step of the e4m3 grid (3 to
+ * 6 %): rounded to the nearest, v could never fall.  Its price is noise: against
  * 32-bit states on Gaussian gradients, v differs by about 17 % at any beta2
  * (a small change seldom moves a code, so a longer memory collects no more
  * noise), m by 9 % at beta1 = 0.9, and the update by 11 % at beta2 = 0.95 and

@@ -290,8 +290,8 @@ def test_eight_bit_states_on_extreme_values():
 
 def test_eight_bit_rounding_keeps_averages():
     """Constant gradients for 120 steps, beta2 = 0.95: the average of v reaches g^2,
-    and of m reaches g (rounded to the nearest, v would stay near its first
-    value, 0.05 g^2).  One rounding has a relative sd of at most 1 / (8 sqrt 6)
+    and of m reaches g (rounded to the nearest, v would stop where a step adds
+    less than half a step of the grid, near 0.6 g^2).  One rounding has a relative sd of at most 1 / (8 sqrt 6)
     (half of a step's probability-weighted square: a step is at most 1/8, the
     mean of f (1 - f) 1/6, and f (1 - f) is at most 1/4: 1/16 bounds it), carried
     1 / sqrt(1 - beta^2): at most 0.2 for v and 0.143 for m.  The mean of n
