@@ -126,7 +126,12 @@ class GradNormBatch(_Prepared):
       nonfinite : int32, 1 if a gradient is infinite or NaN (AdamWBatch then
                   leaves the step out)
     The gradients' addresses are fixed: zero them in place between steps.  Calls of
-    one object must not overlap in time."""
+    one object must not overlap in time.
+
+    Where each rank holds a part of the gradients, run without clipping,
+    all-reduce norm.square() (sum) and nonfinite (max), and write the whole
+    model's norm, scale and flag back into the views: AdamWBatch reads them
+    there."""
 
     def __init__(self, grads: Sequence[torch.Tensor]):
         self.grads = list(grads)   # keep the tensors alive

@@ -291,11 +291,11 @@ def test_eight_bit_states_on_extreme_values():
 def test_eight_bit_rounding_keeps_averages():
     """Constant gradients for 120 steps, beta2 = 0.95: the average of v reaches g^2,
     and of m reaches g (rounded to the nearest, v would stop where a step adds
-    less than half a step of the grid, near 0.6 g^2).  One rounding has a relative sd of at most 1 / (8 sqrt 6)
-    (half of a step's probability-weighted square: a step is at most 1/8, the
-    mean of f (1 - f) 1/6, and f (1 - f) is at most 1/4: 1/16 bounds it), carried
-    1 / sqrt(1 - beta^2): at most 0.2 for v and 0.143 for m.  The mean of n
-    elements is within 6 of its sds with near certainty."""
+    less than half a step of the grid, near 0.6 g^2).  One rounding has a
+    relative sd of at most 1/16: a step of the grid is at most 1/8 of the value,
+    and the variance f (1 - f) of its fraction at most 1/4.  The averages carry
+    that on for 1 / sqrt(1 - beta^2): at most 0.2 for v and 0.143 for m.  The mean
+    of n elements is within 6 of its sds with near certainty."""
     log("8-bit averages")
     n = 1 << 16
     gen = _gen(2)
@@ -478,6 +478,37 @@ def test_clipped_step_uses_the_norm_on_the_device(bits):
     torch.cuda.synchronize()
     assert norm.scale.item() == pytest.approx(0.1, rel=1e-6)
     m.check(m.before, step=5, decay=DECAY, scale=norm.scale.item(), **kw)
+
+
+def test_the_norm_of_parts_is_combined_through_the_views():
+    """Two halves of a model, as two ranks hold them: each one's norm without
+    clipping, the whole's norm, scale and flag written back into the views."""
+    log("norm of parts")
+    parts = [Model([5000, 33], 32, 32, True), Model([4097], 33, 32, True)]
+    norms = [GradNormBatch(m.grads) for m in parts]
+    kw = dict(lr=1e-3, betas=(0.9, 0.95), eps=1e-8)
+    for poison in (False, True):
+        if poison:
+            parts[1].grads[0][3] = math.inf
+        for norm in norms:
+            norm.run()
+        total = (norms[0].norm.square() + norms[1].norm.square()).sqrt()
+        bad = torch.maximum(norms[0].nonfinite, norms[1].nonfinite)
+        for norm in norms:
+            norm.norm.copy_(total)
+            norm.scale.copy_((0.01 / total).clamp(max=1.0))
+            norm.nonfinite.copy_(bad)
+        before = [m.snapshot() for m in parts]
+        for m, norm in zip(parts, norms):
+            m.batch(weight_decay=0.1).run(step=2, norm=norm, **kw)
+        torch.cuda.synchronize()
+        for m, norm, old in zip(parts, norms, before):
+            if poison:
+                assert all(np.array_equal(i, j) for i, j in zip(m.snapshot()["p"], old["p"]))
+            else:
+                want = 0.01 / _norm_of(parts[0].grads + parts[1].grads)
+                assert norm.scale.item() == pytest.approx(want, rel=1e-6) and want < 1
+                m.check(old, step=2, decay=[0.1] * 2, scale=norm.scale.item(), **kw)
 
 
 @pytest.mark.parametrize("apart", [False, True], ids=["in place", "apart"])
