@@ -30,7 +30,7 @@ def _device_ptr(t, what: str, dtypes, numel: int, device) -> int:
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index
             and t.dtype in dtypes and t.numel() == numel and t.is_contiguous()):
         p = t.data_ptr()
-        if p % 16 == 0:
+        if p % 16 == 0 or not numel:
             return p if numel else 0
     _refuse(t, what, dtypes, numel, device)
 
@@ -73,9 +73,13 @@ def _scalar_ptr(t: torch.Tensor, what: str, dtypes, device) -> int:
     return t.data_ptr()
 
 
-# The current stream's handle by device index: 0.1 us, where
-# torch.cuda.current_stream(device).cuda_stream takes 1.9 of a call's 6.5.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _slow_raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream's handle by device index: 0.1 us, where the public form
+# takes 1.9 of a call's 6.5 (a torch built without GPU support lacks the first).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _slow_raw_stream)
 
 
 class _Prepared:
