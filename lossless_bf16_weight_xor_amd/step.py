@@ -189,7 +189,9 @@ class AdamWBatch(_Prepared):
               m_scale, v_scale): uint8 (or float8_e4m3fn) codes, and uint8 (or
               float8_e8m0fnu) scale bytes, one per 32 elements.  They are
               updated in place.  None: zeros, allocated here (the attributes
-              m, v, m_scale, v_scale are the lists in either case).
+              m, v, m_scale, v_scale are the lists in either case).  States
+              allocated here are held for whatever stream a step runs on; tensors
+              that are passed in stay their owner's, as in any torch call.
     weight_decay, lr_scale : a number, or one per tensor
     A tensor that several names share is listed once.  All buffers keep their
     addresses: zero the gradients in place.  Calls of one object must not overlap
@@ -215,6 +217,7 @@ class AdamWBatch(_Prepared):
         places = [_device_ptr(w, "weights", (torch.bfloat16,), n, device)
                   for w, n in zip(self.weights, sizes)]
         parts = 2 if state_bits == 32 else 4
+        self._arenas = []
         if states is None:
             states = self._new_states(sizes, device)
         elif len(states) != parts:
@@ -261,12 +264,16 @@ class AdamWBatch(_Prepared):
 
         def arena(dtype, per):
             flat = torch.zeros(max(at, _SPAN) // per, dtype=dtype, device=device)
+            self._arenas.append(flat)
             return [flat[a // per:a // per + -(-n // per)] for a, n in zip(starts, sizes)]
 
         if self.state_bits == 32:
             return arena(torch.float32, 1), arena(torch.float32, 1)
         return (arena(torch.uint8, 1), arena(torch.uint8, 1), arena(torch.uint8, _SCALE_BLOCK),
                 arena(torch.uint8, _SCALE_BLOCK))
+
+    def _owned(self) -> list:
+        return [self.table, *self._arenas]
 
     def pairs(self) -> list[tuple[torch.Tensor, torch.Tensor]]:
         """(weights, out) per tensor, for CompressBatch; needs an `out` of its own."""
