@@ -101,14 +101,17 @@ class _Prepared:
         """The buffers this object allocated."""
         return [self.table]
 
-    def _call(self, fn, what: str, *args) -> None:
-        """fn(plan, *args, stream) on the current stream of the batch's device."""
-        stream = _raw_stream(self._index)
+    def _hold(self, stream: int) -> None:
+        """Tells the allocator that `stream`, the current one, works on the own buffers."""
         if stream != self._stream0 and not torch.cuda.is_current_stream_capturing():
-            # the allocator may not reuse the buffers while this stream works on them
             s = torch.cuda.current_stream(self.device)
             for t in self._owned():
                 t.record_stream(s)
+
+    def _call(self, fn, what: str, *args) -> None:
+        """fn(plan, *args, stream) on the current stream of the batch's device."""
+        stream = _raw_stream(self._index)
+        self._hold(stream)
         if torch.cuda.current_device() == self._index:
             rc = fn(self._plan_ref, *args, stream)
         else:
@@ -309,5 +312,6 @@ class AdamWBatch(_Prepared):
         if norm is not None:
             if norm.device != self.device:
                 raise ValueError("the norm and the step must be on one device")
+            norm._hold(_raw_stream(self._index))   # it may be at home on another stream
             where = norm.result.data_ptr()
         self._call(self._fn, "bf16d_adamw_step", self._params_ref, where)

@@ -83,3 +83,20 @@ def test_given_states_are_left_to_their_owner(world):
     world.stream = SIDE
     b.run(lr=1e-3, step=1)
     assert world.recorded == {(b.table.untyped_storage().data_ptr(), SIDE)}
+
+
+def test_the_norms_result_is_held_for_the_step_that_reads_it(world):
+    norm = step_module.GradNormBatch([torch.zeros(600)])
+    world.stream = SIDE
+    b = _batch(32)                     # at home on the other stream
+    b.run(lr=1e-3, step=1)
+    assert not world.recorded
+    b.run(lr=1e-3, step=1, norm=norm)
+    assert world.has(norm.result, SIDE)
+    world.stream = HOME
+    world.recorded.clear()
+    b.run(lr=1e-3, step=2, norm=norm)  # the norm's own stream
+    assert not world.has(norm.result, HOME) and world.has(b.table, HOME)
+    world.stream = THIRD
+    norm.run()
+    assert world.has(norm.result, THIRD) and world.has(norm.table, THIRD)
