@@ -102,11 +102,15 @@ class _Prepared:
         return [self.table]
 
     def _hold(self, stream: int) -> None:
-        """Tells the allocator that `stream`, the current one, works on the own buffers."""
-        if stream != self._stream0 and not torch.cuda.is_current_stream_capturing():
-            s = torch.cuda.current_stream(self.device)
-            for t in self._owned():
-                t.record_stream(s)
+        """Tells the allocator that `stream`, the device's current one, works on the own
+        buffers (not in a capture: a graph needs the object alive anyway)."""
+        if stream == self._stream0:
+            return
+        with torch.cuda.device(self.device):   # the capture asked for is the current device's
+            if not torch.cuda.is_current_stream_capturing():
+                s = torch.cuda.current_stream()
+                for t in self._owned():
+                    t.record_stream(s)
 
     def _call(self, fn, what: str, *args) -> None:
         """fn(plan, *args, stream) on the current stream of the batch's device."""

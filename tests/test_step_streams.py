@@ -100,3 +100,15 @@ def test_the_norms_result_is_held_for_the_step_that_reads_it(world):
     world.stream = THIRD
     norm.run()
     assert world.has(norm.result, THIRD) and world.has(norm.table, THIRD)
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_capture_is_looked_for_on_the_batchs_device(world, capturing):
+    """Another device is current: whether its stream is captured says nothing."""
+    b = _batch(32)
+    world.device = 1
+    world.capturing = {b._index if capturing else 1}
+    world.stream = SIDE
+    b.run(lr=1e-3, step=1)
+    assert world.has(b.table, SIDE) != capturing
+    assert world.device == 1
