@@ -58,8 +58,11 @@ typedef struct bf16d_grad {
  *               inputs give equal bits.
  *   scale     : grad_scale * min(1, max_norm / norm): the factor that turns a
  *               gradient as stored into the one the step uses.
- *   nonfinite : 1 if any gradient is infinite or NaN (norm and scale are
- *               then of no use), else 0. */
+ *   nonfinite : 1 if any gradient, as stored, is infinite or NaN (norm and scale
+ *               are then of no use), else 0.  scale is finite in any case, but
+ *               scale * gradient, and its square in v, are formed in fp32: they
+ *               can overflow from gradients of 3.4e38 and 1.8e19 on, which the
+ *               flag does not cover (with a max_norm below 1.8e19 they cannot). */
 typedef struct bf16d_norm_result {
     double   norm;
     float    scale;
@@ -74,7 +77,7 @@ int bf16d_grad_norm_prepare(const bf16d_grad *grads, uint32_t count, void *table
                             size_t table_bytes, bf16d_norm_result *result, hipStream_t stream,
                             bf16d_step_plan *plan);
 
-/* max_norm: above 0; infinity for no clipping.  grad_scale: finite; what a
+/* max_norm: above 0; infinity for no clipping.  grad_scale: finite in fp32; what a
  * stored gradient is multiplied by (1 / the number of accumulated batches,
  * for example). */
 int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_scale,

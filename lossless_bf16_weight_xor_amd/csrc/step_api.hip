@@ -280,7 +280,9 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
     Plan p;
     int rc = read_plan(plan, kNormMagic, p);
     if (rc != BF16D_OK) return rc;
-    if (!(max_norm > 0.0) || !std::isfinite(grad_scale)) return BF16D_EINVAL;
+    // The step multiplies by the scale in fp32.  Clipping only makes it smaller, so
+    // where grad_scale is finite there, the scale is.
+    if (!(max_norm > 0.0) || !std::isfinite(float(grad_scale))) return BF16D_EINVAL;
     rc = check_device(p, stream);
     if (rc != BF16D_OK) return rc;
     NormArgs a{};

@@ -24,6 +24,7 @@ from . import _check_rc
 _GRAD_TYPES = {torch.bfloat16: _native.GRAD_BF16, torch.float32: _native.GRAD_F32}
 _SPAN = 512          # elements: an arena's tensors start on multiples of this
 _SCALE_BLOCK = 32    # elements that share a scale byte
+_F32_END = 2.0 ** 128 - 2.0 ** 103   # the least number that is infinite in fp32
 
 
 def _device_ptr(t, what: str, dtypes, numel: int, device) -> int:
@@ -173,9 +174,9 @@ class GradNormBatch(_Prepared):
 
     def run(self, max_norm: float = math.inf, grad_scale: float = 1.0) -> None:
         """max_norm: above 0, infinity for no clipping.  grad_scale: what the
-        stored gradients are multiplied by (finite)."""
-        if not max_norm > 0 or not math.isfinite(grad_scale):
-            raise ValueError("max_norm must be above 0 and grad_scale finite")
+        stored gradients are multiplied by (finite in fp32)."""
+        if not max_norm > 0 or not abs(grad_scale) < _F32_END:
+            raise ValueError("max_norm must be above 0 and grad_scale finite in fp32")
         self._call(self._fn, "bf16d_grad_norm", max_norm, grad_scale)
 
 
