@@ -71,8 +71,10 @@ typedef struct bf16d_norm_result {
 
 size_t bf16d_grad_norm_table_bytes(uint64_t total_n, uint32_t count);
 
-/* `result` receives the outcome of every later call on this plan.  It may not
- * overlap the gradients or the table. */
+/* `result` receives the outcome of every later call on this plan, and is not
+ * written here: before the first call it holds what the caller put there (a
+ * nonfinite of 1 makes a step that reads it too early one that is left out).  It
+ * may not overlap the gradients or the table. */
 int bf16d_grad_norm_prepare(const bf16d_grad *grads, uint32_t count, void *table,
                             size_t table_bytes, bf16d_norm_result *result, hipStream_t stream,
                             bf16d_step_plan *plan);

@@ -136,7 +136,7 @@ class GradNormBatch(_Prepared):
       scale     : float32, grad_scale * min(1, max_norm / norm), what
                   AdamWBatch multiplies the gradients by
       nonfinite : int32, 1 if a gradient is infinite or NaN (AdamWBatch then
-                  leaves the step out)
+                  leaves the step out), and before the first run
     The gradients' addresses are fixed: zero them in place between steps.  Calls of
     one object must not overlap in time.
 
@@ -161,6 +161,7 @@ class GradNormBatch(_Prepared):
         words = self.result.view(torch.int32)
         self.scale = words[2:3].view(torch.float32)[0]
         self.nonfinite = words[3]
+        self.nonfinite.fill_(1)   # nothing to scale by before the first run
         lib = _native.lib()
         self._fn = lib.bf16d_grad_norm
         total = sum(g.numel() for g in self.grads)

@@ -34,3 +34,24 @@ def test_grad_scale_up_to_the_largest_fp32_number():
         assert norm.nonfinite.item() == 0
         want = abs(good) * math.hypot(2.0 ** -130, 2.0 ** -140)
         assert norm.norm.item() == pytest.approx(want, rel=1e-14)
+
+
+@pytest.mark.parametrize("bits,master", [(32, True), (8, True), (8, False)])
+def test_a_norm_that_has_not_run_leaves_the_step_out(bits, master):
+    """Its scale is no factor yet: a step with it may not take the gradients for zeros."""
+    log(f"norm that has not run, bits={bits} master={master}")
+    m = Model([5000, 33], 1, bits, master, apart=True)
+    norm, batch = GradNormBatch(m.grads), m.batch(weight_decay=0.1)
+    batch.run(lr=1e-3, step=1, norm=norm)
+    torch.cuda.synchronize()
+    now = m.snapshot()
+    assert all(_same(a, b) for a, b in zip(now["s"], m.before["s"]))
+    assert _same(now["p"], m.before["p"])
+    assert _same(now["out"], [ref.bf16_bits_nearest(x.astype(np.float64)) for x in m.before["p"]]
+                 if master else m.before["w"])
+    # and once it has run, it is a step like any other
+    kw = dict(lr=1e-3, betas=(0.9, 0.95), eps=1e-8, step=1)
+    norm.run()
+    batch.run(norm=norm, **kw)
+    torch.cuda.synchronize()
+    m.check(m.before, decay=[0.1] * 2, **kw)
