@@ -399,8 +399,9 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
     }
 }
 
-void launch_adamw(const AdamArgs &a, uint32_t state_bits, uint32_t lds_bytes, hipStream_t stream) {
-    if (a.groups == 0) return;
+hipError_t launch_adamw(const AdamArgs &a, uint32_t state_bits, uint32_t lds_bytes,
+                        hipStream_t stream) {
+    if (a.groups == 0) return hipSuccess;
     const uint32_t grid = a.groups < kAdamGrid ? a.groups : kAdamGrid;
     // v_sqrt_f32 takes a denormal v for 0.  Its root, below 2^-63, times root2,
     // which 1 / sqrt(rest2) bounds, is then lost beside eps: less than u = 2^-24
@@ -408,7 +409,7 @@ void launch_adamw(const AdamArgs &a, uint32_t state_bits, uint32_t lds_bytes, hi
     const bool exact = a.eps * 0x1p39 < 1.0 / sqrt((double)a.rest2);
     auto *kernel = state_bits == 8 ? (exact ? adamw_kernel<8, true> : adamw_kernel<8, false>)
                                    : (exact ? adamw_kernel<32, true> : adamw_kernel<32, false>);
-    kernel<<<grid, kAdamThreads, lds_bytes, stream>>>(a);
+    return launch_one(kernel, grid, kAdamThreads, a, lds_bytes, stream);
 }
 
 }  // namespace bf16d

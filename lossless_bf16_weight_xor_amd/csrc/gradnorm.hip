@@ -128,11 +128,11 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormArgs a) {
     }
 }
 
-void launch_grad_norm(const NormArgs &a, hipStream_t stream) {
+hipError_t launch_grad_norm(const NormArgs &a, hipStream_t stream) {
     const uint32_t grid =
         (uint32_t)(a.chunks < kNormGrid ? (a.chunks ? a.chunks : 1) : kNormGrid);
     auto *kernel = a.kept ? grad_norm_kernel<true> : grad_norm_kernel<false>;
-    kernel<<<grid, kThreads, 0, stream>>>(a);
+    return launch_one(kernel, grid, kThreads, a, 0, stream);
 }
 
 }  // namespace bf16d

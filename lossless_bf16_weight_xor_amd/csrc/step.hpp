@@ -145,7 +145,19 @@ __device__ __forceinline__ T load_constant(const T *p) {
     return __builtin_bit_cast(T, x);
 }
 
-void launch_grad_norm(const NormArgs &a, hipStream_t stream);
-void launch_adamw(const AdamArgs &a, uint32_t state_bits, uint32_t lds_bytes, hipStream_t stream);
+// Launches a kernel of one argument and gives back the launch's own status:
+// hipGetLastError would report an error that some earlier call left behind, of
+// a step that has been enqueued.
+template <typename Args>
+hipError_t launch_one(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &a,
+                      uint32_t lds_bytes, hipStream_t stream) {
+    void *args[] = {const_cast<Args *>(&a)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), args,
+                           lds_bytes, stream);
+}
+
+hipError_t launch_grad_norm(const NormArgs &a, hipStream_t stream);
+hipError_t launch_adamw(const AdamArgs &a, uint32_t state_bits, uint32_t lds_bytes,
+                        hipStream_t stream);
 
 }  // namespace bf16d

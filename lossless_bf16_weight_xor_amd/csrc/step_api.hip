@@ -295,8 +295,7 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
     a.kept = p.kept;
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
-    launch_grad_norm(a, stream);
-    return hipGetLastError() == hipSuccess ? BF16D_OK : BF16D_EHIP;
+    return launch_grad_norm(a, stream) == hipSuccess ? BF16D_OK : BF16D_EHIP;
 }
 
 int bf16d_adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t state_bits,
@@ -346,8 +345,8 @@ int bf16d_adamw_step(const bf16d_step_plan *plan, const bf16d_adamw_params *para
     a.seed = P.seed;
     a.step = P.step;
     a.groups = uint32_t(p.chunks) * kAdamSplit;
-    launch_adamw(a, p.state_bits, p.lds_bytes, stream);
-    return hipGetLastError() == hipSuccess ? BF16D_OK : BF16D_EHIP;
+    return launch_adamw(a, p.state_bits, p.lds_bytes, stream) == hipSuccess ? BF16D_OK
+                                                                            : BF16D_EHIP;
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 """Calls of the optimizer step and the gradient norm on the GPU that go beside their
 plain use: numbers at the border of fp32, a norm without a result, copies in
 place, errors and steps left out around them."""
+import ctypes
 import math
 
 import numpy as np
@@ -55,3 +56,32 @@ def test_a_norm_that_has_not_run_leaves_the_step_out(bits, master):
     batch.run(norm=norm, **kw)
     torch.cuda.synchronize()
     m.check(m.before, decay=[0.1] * 2, **kw)
+
+
+def _hip_runtime():
+    """The HIP runtime that this process has loaded."""
+    with open("/proc/self/maps") as f:
+        paths = {line.split()[-1] for line in f if "libamdhip64" in line}
+    assert len(paths) == 1, paths
+    return ctypes.CDLL(paths.pop())
+
+
+def test_an_error_left_by_another_call_is_not_the_steps():
+    """A refused runtime call leaves its error behind (here: a device that is not
+    there); a norm and a step after it do their work and say so."""
+    log("error of another call")
+    m = Model([5000, 33], 1, 32, True)
+    norm, batch = GradNormBatch(m.grads), m.batch(weight_decay=0.0)
+    kw = dict(lr=1e-3, betas=(0.9, 0.95), eps=1e-8, step=1)
+    torch.cuda.synchronize()
+    hip = _hip_runtime()
+    try:
+        assert hip.hipSetDevice(99) != 0
+        norm.run()
+        assert hip.hipSetDevice(99) != 0
+        batch.run(norm=norm, **kw)
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert norm.nonfinite.item() == 0
+    m.check(m.before, decay=[0.0] * 2, **kw)
