@@ -12,6 +12,7 @@ CompressBatch.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import math
 from typing import Sequence
@@ -286,8 +287,18 @@ class AdamWBatch(_Prepared):
 
     def pairs(self) -> list[tuple[torch.Tensor, torch.Tensor]]:
         """(weights, out) per tensor, for CompressBatch; needs an `out` of its own."""
-        if self.out is self.weights:
-            raise ValueError("the step is done in place: there is no old copy to compare with")
+        ends = lambda t: (t.data_ptr(), t.data_ptr() + 2 * t.numel())
+        # the new copies are apart from each other: by their starts, and so by their ends
+        new = sorted(ends(t) for t in self.out if t.numel())
+
+        def written(t):
+            lo, hi = ends(t)
+            k = bisect.bisect_left(new, (hi,))   # the new copies before it begin below hi
+            return t.numel() and k and new[k - 1][1] > lo
+
+        if self.out is self.weights or any(map(written, self.weights)):
+            raise ValueError("the step writes over the weights: there is no old copy to "
+                             "compare with")
         return list(zip(self.weights, self.out))
 
     def run(self, lr, step, betas: tuple[float, float] = (0.9, 0.95), eps: float = 1e-8,

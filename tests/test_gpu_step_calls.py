@@ -85,3 +85,21 @@ def test_an_error_left_by_another_call_is_not_the_steps():
     torch.cuda.synchronize()
     assert norm.nonfinite.item() == 0
     m.check(m.before, decay=[0.0] * 2, **kw)
+
+
+def test_pairs_of_copies_that_share_memory_are_refused():
+    """(old, new) means nothing where the step has written the old copy: the same
+    tensors given twice, or one tensor's new copy in the place of another's old one."""
+    log("pairs that share memory")
+    m = Model([64, 40, 0], 7, 32, True)
+    kw = dict(masters=m.masters, states=m.states)
+    for out in (None, m.weights, [w.view(-1) for w in m.weights],
+                [torch.empty_like(m.weights[0]), m.weights[0][:40], m.weights[2]],
+                [torch.empty_like(m.weights[0]), m.weights[0][16:56], m.weights[2]]):
+        with pytest.raises(ValueError, match="old copy"):
+            AdamWBatch(m.weights, m.grads, out=out, **kw).pairs()
+    both = torch.empty(2 * 64, dtype=torch.bfloat16, device=DEV)   # neighbours, but apart
+    a, b = both[:64], both[64:]
+    for w, out in (([a], [b]), ([b], [a])):
+        (old, new), = AdamWBatch(w, m.grads[:1], out=out, masters=m.masters[:1]).pairs()
+        assert old is w[0] and new is out[0]
