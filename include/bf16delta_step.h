@@ -129,10 +129,10 @@ int bf16d_grad_norm(const bf16d_step_plan *plan, double max_norm, double grad_sc
  * The rounding is stochastic because a step lowers v by at most 1 - beta2 of
  * itself, at beta2 = 0.999 far less than half a step of the e4m3 grid (3 to
  * 6 %): rounded to the nearest, v could never fall.  Its price is noise: against
- * 32-bit states on Gaussian gradients, v differs by about 17 % at any beta2
- * (a small change seldom moves a code, so a longer memory collects no more
- * noise), m by 9 % at beta1 = 0.9, and the update by 11 % at beta2 = 0.95 and
- * 14 % at 0.999 (its mean by 1 to 2 %).
+ * 32-bit states on Gaussian gradients, v differs by 13, 18 and 21 % (rms) at beta2
+ * = 0.95, 0.99 and 0.999 (a longer memory collects hardly more, since a small
+ * change seldom moves a code: 33 % is a bound for all of these), m by 9 % at
+ * beta1 = 0.9, and the update by 11, 13 and 14 % (its mean by 1 to 2 %).
  *
  * Random numbers: element i of job j has number e = start_j + i, start_j the
  * sum of the earlier jobs' n, each rounded up to a multiple of 512.  With

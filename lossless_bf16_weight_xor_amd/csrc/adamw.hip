@@ -154,7 +154,8 @@ __device__ __forceinline__ u32x2 random_bf16(const f32x4 &x, const uint32_t (&ra
     return r;
 }
 
-// e4m3 codes times the block's scale, exact for every byte from 0 to 254
+// e4m3 codes times the block's scale, exact for every byte from 0 to 254 whose
+// value fp32 holds (2^128, the code of 256 under byte 247, and more become infinite)
 __device__ __forceinline__ f32x4 decode(uint32_t codes, uint32_t scale_byte) {
     const float s = __uint_as_float(scale_byte << 23);
     const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, s, false);
