@@ -186,7 +186,8 @@ int bf16d_adamw_prepare(const bf16d_adamw_job *jobs, uint32_t count, uint32_t st
  * scale multiplies the gradients, or NULL.  If its nonfinite flag is set, the
  * step is left out: masters and states keep their values, and out receives the
  * weights as they are (bf16(master), or a copy of `weights`).  The caller
- * advances the step number. */
+ * advances the step number, by 1 - nonfinite so that a step left out does not
+ * count. */
 int bf16d_adamw_step(const bf16d_step_plan *plan, const bf16d_adamw_params *params,
                      const bf16d_norm_result *norm, hipStream_t stream);
 

@@ -308,7 +308,9 @@ class AdamWBatch(_Prepared):
         lr   : a number, or a float32 device tensor that the kernel reads
         step : the step's number from 1, or an int64 device tensor that the
                kernel reads (for graphs: advance it in the graph, and keep
-               both tensors alive as long as it)
+               both tensors alive as long as it).  A step that is left out is no
+               step: step.add_(1 - norm.nonfinite) between the norm and this
+               call counts only those that are made.
         seed : of the stochastic rounding, with the step's number
         norm : a GradNormBatch that has run on these gradients: its scale
                multiplies them, and the step is left out if it found them not finite"""

@@ -11,7 +11,7 @@ import torch
 from lossless_bf16_weight_xor_amd import AdamWBatch, GradNormBatch
 from tests import step_reference as ref
 from tests.gpu_util import log
-from tests.test_gpu_step import DEV, Model
+from tests.test_gpu_step import DEV, Model, _gen, _normal
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,40 @@ def test_pairs_of_copies_that_share_memory_are_refused():
     for w, out in (([a], [b]), ([b], [a])):
         (old, new), = AdamWBatch(w, m.grads[:1], out=out, masters=m.masters[:1]).pairs()
         assert old is w[0] and new is out[0]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_left_out_step_in_a_graph_need_not_advance_the_number(bits):
+    """step.add_(1 - norm.nonfinite) between the norm and the step: a replay whose
+    gradients are not finite changes nothing, the number included, and the next
+    one is what an eager loop that skips the batch does."""
+    log(f"left out in a graph, bits={bits}")
+    sizes = [20011, 333, 4096]
+    a, b = (Model(sizes, 63, bits, True) for _ in range(2))
+    norms = [GradNormBatch(x.grads) for x in (a, b)]
+    batches = [x.batch() for x in (a, b)]
+    step = torch.tensor(0, dtype=torch.int64, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norms[0].run(max_norm=0.5)
+        step.add_(1 - norms[0].nonfinite)
+        batches[0].run(lr=1e-3, step=step, seed=4, norm=norms[0])
+    gen = _gen(6)
+    t = 0
+    for poison in (False, True, False, True, True, False):
+        for x, y in zip(a.grads, b.grads):
+            x.copy_(_normal(x.numel(), gen, 1e-2))
+            y.copy_(x)
+        if poison:
+            a.grads[1][7] = math.nan
+        graph.replay()
+        if not poison:
+            t += 1
+            norms[1].run(max_norm=0.5)
+            batches[1].run(lr=1e-3, step=t, seed=4, norm=norms[1])
+        torch.cuda.synchronize()
+        assert step.item() == t
+        x, y = a.snapshot(), b.snapshot()
+        assert _same(x["w"], y["w"]) and _same(x["p"], y["p"])
+        assert all(_same(i, j) for i, j in zip(x["s"], y["s"]))
