@@ -6,7 +6,7 @@ CompressBatch.
     norm = GradNormBatch(grads)
     step = AdamWBatch(weights, grads, masters=masters, out=spare)
     for t in range(1, steps + 1):
-        ...                                   # backward into grads
+        ...                                   # zero grads in place, backward into them
         norm.run(max_norm=1.0)
         step.run(lr=1e-5, step=t, norm=norm)  # spare holds the new weights
 """
@@ -138,8 +138,10 @@ class GradNormBatch(_Prepared):
                   AdamWBatch multiplies the gradients by
       nonfinite : int32, 1 if a gradient is infinite or NaN (AdamWBatch then
                   leaves the step out), and before the first run
-    The gradients' addresses are fixed: zero them in place between steps.  Calls of
-    one object must not overlap in time.
+    The gradients' addresses are fixed: zero them in place between steps
+    (zero_grad(set_to_none=False); torch's default drops the tensors, this object
+    would go on reading the old ones, and it cannot tell).  Gradients that have
+    moved want a new object.  Calls of one object must not overlap in time.
 
     Where each rank holds a part of the gradients, run without clipping,
     all-reduce norm.square() (sum) and nonfinite (max), and write the whole
@@ -204,9 +206,11 @@ class AdamWBatch(_Prepared):
               that are passed in stay their owner's, as in any torch call.
     weight_decay, lr_scale : a number, or one per tensor
     A tensor that several names share is listed once.  All buffers keep their
-    addresses: zero the gradients in place.  Calls of one object must not overlap
-    in time, nor replays of graphs that hold them (keep it alive as long as
-    those)."""
+    addresses: zero the gradients in place (zero_grad(set_to_none=False)), or, after
+    torch's default has dropped them, prepare a new batch over the new ones with
+    this one's lists as its states: nothing here can tell that a gradient moved.
+    Calls of one object must not overlap in time, nor replays of graphs that
+    hold them (keep it alive as long as those)."""
 
     def __init__(self, weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  masters: Sequence[torch.Tensor] | None = None,

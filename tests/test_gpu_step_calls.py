@@ -140,3 +140,30 @@ def test_a_left_out_step_in_a_graph_need_not_advance_the_number(bits):
         x, y = a.snapshot(), b.snapshot()
         assert _same(x["w"], y["w"]) and _same(x["p"], y["p"])
         assert all(_same(i, j) for i, j in zip(x["s"], y["s"]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_that_moved_are_prepared_anew(bits):
+    """Parameters whose gradients were set to None and made again: batches prepared
+    over the new ones, with the old batch's states, go on where it stopped."""
+    log(f"moved gradients, bits={bits}")
+    sizes = [5000, 33]
+    moved, fixed = (Model(sizes, 64, bits, True) for _ in range(2))
+    kept = fixed.batch()
+    names = ("m", "v", "m_scale", "v_scale")[:2 if bits == 32 else 4]
+    last = moved.batch()
+    gen = _gen(8)
+    for t in range(1, 4):
+        for j, g in enumerate(fixed.grads):
+            g.copy_(_normal(sizes[j], gen, 1e-2))
+            moved.grads[j] = g.clone()
+        norm = GradNormBatch(moved.grads)
+        last = AdamWBatch(moved.weights, moved.grads, masters=moved.masters, state_bits=bits,
+                          states=[getattr(last, x) for x in names])
+        norm.run(max_norm=0.1)
+        last.run(lr=1e-3, step=t, seed=2, norm=norm)
+        kept.run(lr=1e-3, step=t, seed=2, norm=norm)      # of equal gradients
+    torch.cuda.synchronize()
+    x, y = moved.snapshot(), fixed.snapshot()
+    assert _same(x["w"], y["w"]) and _same(x["p"], y["p"])
+    assert all(_same(i, j) for i, j in zip(x["s"], y["s"]))
