@@ -11,12 +11,17 @@ namespace bf16d {
 
 // ---- gradient norm -------------------------------------------------------------
 // Elements a workgroup reads per turn (32 bytes a thread in bf16, 64 in fp32),
-// and workgroups at most, four for each of the 256 CUs.  Workgroup b always takes
-// chunks b, b + grid, ... and leaves one partial sum, so the grouping of the
-// sums depends on the sizes alone.  1.75e9 bf16 gradients: 490 us (7.1 TB/s);
+// and workgroups at most, four for each of the 256 CUs.  Workgroup b takes turns
+// b, b + grid, ..., counted from the first chunk, or from the last one where some
+// are kept, and leaves one partial sum, so the grouping of the sums depends on
+// the sizes alone.  1.75e9 bf16 gradients: 490 us (7.1 TB/s);
 // with 2048 workgroups 536, with 768 569, with 512 814; with 8192 elements a
 // turn 502 (1024 workgroups) and 484 (768), which leaves fewer turns to share
-// out in smaller batches; with 2048 elements 741.
+// out in smaller batches; with 2048 elements 741.  These were chosen on large
+// batches.  In middle ones a fixed time shows that grows with the workgroups up
+// to their most: 4.7 us for 2.7e5 bf16 elements (66 workgroups), 9.5 for 2e6
+// (489), 17 for 8e6 and 23 for 3.2e7 (1024), where the launch and the read take
+// 5, 5, 7 and 14.
 constexpr uint32_t kNormChunk = 4096;
 constexpr uint32_t kNormGrid = 1024;
 // In batches up to kNormKeptTotal the chunks are read from the last one back to

@@ -314,7 +314,8 @@ class AdamWBatch(_Prepared):
                kernel reads (for graphs: advance it in the graph, and keep
                both tensors alive as long as it).  A step that is left out is no
                step: step.add_(1 - norm.nonfinite) between the norm and this
-               call counts only those that are made.
+               call counts only those that are made.  Device tensors cost 1 to 3 %
+               of a step's time, but a third with 8-bit states and no masters
         seed : of the stochastic rounding, with the step's number
         norm : a GradNormBatch that has run on these gradients: its scale
                multiplies them, and the step is left out if it found them not finite"""
