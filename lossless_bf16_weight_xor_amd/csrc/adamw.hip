@@ -358,7 +358,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs a) {
     }
     // Numbers in device words cost every wave its own double-precision arithmetic,
     // which shows where the vector units are nearly full: 2.0e8 elements with 8-bit
-    // states and no master copies take 444 us for 327, in the other forms 1 to 3 %
+    // states and no master copies take 444 us for 329, in the other forms 1 to 3 %
     // more.
     StepNumbers n = a.numbers;
     if (a.lr_device || a.step_device) {
