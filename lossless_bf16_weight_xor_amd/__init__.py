@@ -15,8 +15,10 @@ cross-region RL", section "Using ARCv3":
 
 The wire format is this project's own "bf16delta_v1", not ARCv3's.
 
-On the trainer's side, AdamWBatch and GradNormBatch (bf16delta_step.h) make the
-new weights that are compressed.
+On the trainer's side, TokenLogProbs, PolicyLoss and RouterBalance
+(bf16delta_loss.h) turn a model's logits into the loss and its gradients, and
+AdamWBatch and GradNormBatch (bf16delta_step.h) make the new weights that are
+compressed.
 """
 from __future__ import annotations
 
@@ -38,7 +40,7 @@ __all__ = ["delta_compress", "delta_decompress", "compress_batch", "decompress_b
            "decompress_remapped", "race_compress", "race_decompress", "codec_available",
            "RaceFrame", "DEFAULT_RACE", "FormatError", "ChecksumError",
            "CapacityError", "max_payload_bytes", "workspace_bytes", "FORMAT", "AdamWBatch",
-           "GradNormBatch"]
+           "GradNormBatch", "TokenLogProbs", "PolicyLoss", "RouterBalance"]
 
 
 class FormatError(ValueError):
@@ -665,3 +667,5 @@ def race_decompress(frames, threads: int = 0, pin: bool = False) -> list[torch.T
 
 # the trainer's step that makes the new weights
 from .step import AdamWBatch, GradNormBatch  # noqa: E402
+# the losses of a policy update
+from .loss import PolicyLoss, RouterBalance, TokenLogProbs  # noqa: E402

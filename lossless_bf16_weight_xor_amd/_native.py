@@ -33,6 +33,13 @@ EXPORTED = ("bf16d_max_payload_bytes", "bf16d_workspace_bytes",
 STEP_EXPORTED = ("bf16d_grad_norm_table_bytes", "bf16d_grad_norm_prepare", "bf16d_grad_norm",
                  "bf16d_adamw_table_bytes", "bf16d_adamw_prepare", "bf16d_adamw_step")
 GRAD_BF16, GRAD_F32 = 0, 1
+# the losses, declared in bf16delta_loss.h
+LOSS_EXPORTED = ("bf16d_logprob_workspace_bytes", "bf16d_logprob", "bf16d_logprob_backward",
+                 "bf16d_policy_loss_workspace_bytes", "bf16d_policy_loss",
+                 "bf16d_balance_workspace_bytes", "bf16d_balance", "bf16d_balance_backward")
+LOGITS_BF16, LOGITS_F32 = 0, 1
+IDS_I64, IDS_I32 = 0, 1
+MAX_VOCAB, MAX_TOP, MAX_EXPERTS = 1 << 28, 64, 1024
 # the benchmark's measurement aids, in their own library (bf16delta_probe.h)
 PROBE_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbf16delta_probe.so")
 PROBE_EXPORTED = ("bf16d_probe_read", "bf16d_probe_inplace", "bf16d_probe_write")
@@ -117,6 +124,46 @@ class AdamWParams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_uint64), ("seed", ctypes.c_uint64),
                 ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p)]
+
+
+def _fields(**types):
+    kinds = {"p": ctypes.c_void_p, "q": ctypes.c_uint64, "i": ctypes.c_uint32,
+             "d": ctypes.c_double}
+    return [(name, kinds[k]) for name, k in types.items()]
+
+
+# (a bf16d_rows member is three fields here: address, outer and inner stride)
+class LogprobJob(ctypes.Structure):
+    _fields_ = _fields(logits="p", logits_outer="q", logits_inner="q", tokens="p",
+                       tokens_outer="q", tokens_inner="q", outer="q", inner="q", vocab="i",
+                       logits_dtype="i", token_dtype="i", top="i", temperature="d", logp="p",
+                       entropy="p", stats="p", top_ids="p", top_logp="p")
+
+
+class LogprobGradJob(ctypes.Structure):
+    _fields_ = _fields(logits="p", logits_outer="q", logits_inner="q", tokens="p",
+                       tokens_outer="q", tokens_inner="q", out="p", out_outer="q",
+                       out_inner="q", outer="q", inner="q", vocab="i", logits_dtype="i",
+                       token_dtype="i", reserved="i", stats="p", grad_logp="p",
+                       grad_entropy="p")
+
+
+class PolicyJob(ctypes.Structure):
+    _fields_ = _fields(logp="p", old="p", advantages="p", weights="p", ref="p", entropy="p",
+                       grad_logp="p", grad_entropy="p", n="q", clip_low="d", clip_high="d",
+                       kl_coef="d", entropy_coef="d", scale="d")
+
+
+class BalanceJob(ctypes.Structure):
+    _fields_ = _fields(logits="p", chosen="p", mask="p", rows="q", logits_stride="q",
+                       chosen_stride="q", experts="i", choices="i", logits_dtype="i",
+                       chosen_dtype="i", balance_coef="d", z_coef="d", counts="p")
+
+
+class BalanceGradJob(ctypes.Structure):
+    _fields_ = _fields(logits="p", out="p", mask="p", rows="q", logits_stride="q",
+                       out_stride="q", experts="i", logits_dtype="i", balance_coef="d",
+                       z_coef="d", scale="d", counts="p", tokens="p", result="p")
 
 
 RESULT_BYTES = ctypes.sizeof(Result)
@@ -222,6 +269,22 @@ def lib():
         L.bf16d_adamw_step.argtypes = [ctypes.POINTER(StepPlan), ctypes.POINTER(AdamWParams), vp,
                                        vp]
         L.bf16d_adamw_step.restype = ctypes.c_int
+        L.bf16d_logprob_workspace_bytes.argtypes = [u64, u32, u32]
+        L.bf16d_logprob_workspace_bytes.restype = sz
+        L.bf16d_logprob.argtypes = [ctypes.POINTER(LogprobJob), vp, sz, vp]
+        L.bf16d_logprob.restype = ctypes.c_int
+        L.bf16d_logprob_backward.argtypes = [ctypes.POINTER(LogprobGradJob), vp]
+        L.bf16d_logprob_backward.restype = ctypes.c_int
+        L.bf16d_policy_loss_workspace_bytes.argtypes = []
+        L.bf16d_policy_loss_workspace_bytes.restype = sz
+        L.bf16d_policy_loss.argtypes = [ctypes.POINTER(PolicyJob), vp, vp, sz, vp]
+        L.bf16d_policy_loss.restype = ctypes.c_int
+        L.bf16d_balance_workspace_bytes.argtypes = [u32]
+        L.bf16d_balance_workspace_bytes.restype = sz
+        L.bf16d_balance.argtypes = [ctypes.POINTER(BalanceJob), vp, vp, sz, vp]
+        L.bf16d_balance.restype = ctypes.c_int
+        L.bf16d_balance_backward.argtypes = [ctypes.POINTER(BalanceGradJob), vp]
+        L.bf16d_balance_backward.restype = ctypes.c_int
         _lib = L
     return _lib
 

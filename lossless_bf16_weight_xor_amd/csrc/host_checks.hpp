@@ -1,10 +1,13 @@
 // host_checks.hpp -- argument checks shared by the host side of the C ABI.
 #pragma once
 
+#include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
 #include <vector>
+
+#include "bf16delta.h"
 
 namespace bf16d {
 
@@ -33,6 +36,28 @@ inline bool ranges_disjoint(std::vector<Range> &v) {
         if (r.written) reach_written = std::max(reach_written, r.hi);
     }
     return true;
+}
+
+inline void add_range(std::vector<Range> &v, const void *p, uint64_t bytes, bool written) {
+    v.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
+}
+
+inline bool device_of(hipStream_t stream, int32_t &out) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return false;
+    out = dev;
+    return true;
+}
+
+// BF16D_OK if `stream` belongs to the current device
+inline int stream_on_current(hipStream_t stream, int32_t &dev) {
+    if (!device_of(stream, dev)) return BF16D_EHIP;
+    if (stream) {
+        hipDevice_t sdev = -1;
+        if (hipStreamGetDevice(stream, &sdev) != hipSuccess) return BF16D_EHIP;
+        if (sdev != dev) return BF16D_EINVAL;
+    }
+    return BF16D_OK;
 }
 
 }  // namespace bf16d

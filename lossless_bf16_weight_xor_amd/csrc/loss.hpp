@@ -1,0 +1,152 @@
+// loss.hpp -- shared definitions of the loss kernels and the host code that
+// launches them (include/bf16delta_loss.h).
+#pragma once
+
+#include <math.h>
+
+#include "bf16delta_loss.h"
+#include "internal.hpp"
+#include "step.hpp"
+
+namespace bf16d {
+
+// ---- log probabilities --------------------------------------------------------
+// A row is read in turns: four 16-byte vectors a thread.  Rows are cut into
+// parts of whole turns, one workgroup each, where there are fewer rows than
+// kLogprobGroups.
+constexpr uint32_t kTurnVectors = 4 * kThreads;
+constexpr uint32_t kLogprobGroups = 1024;
+constexpr uint32_t vector_elems(uint32_t dtype) { return dtype == BF16D_LOGITS_F32 ? 4 : 8; }
+inline uint32_t turns_of(uint32_t vocab, uint32_t dtype) {
+    const uint32_t per = kTurnVectors * vector_elems(dtype);
+    return (vocab + per - 1) / per;
+}
+
+// Rows of a call, as the device sees them.
+struct RowSet {
+    void *data;
+    uint64_t outer_stride, inner_stride;
+};
+
+struct LogprobArgs {
+    RowSet logits, tokens;
+    uint32_t rows, inner, vocab, token_i32, top;
+    uint32_t parts, part_turns;   // workgroups of a row, turns of each
+    float scale;                  // log2(e) / temperature
+    float inv_t;
+    float *logp, *entropy;
+    bf16d_row_stats *stats;
+    int64_t *top_ids;
+    float *top_logp;
+    uint64_t *partial;   // (2 + top) words of each part of each row
+    uint32_t *done;      // of each row
+};
+hipError_t launch_logprob(const LogprobArgs &a, bool f32, hipStream_t stream);
+
+struct LogprobGradArgs {
+    RowSet logits, tokens, out;
+    uint32_t rows, inner, vocab, token_i32;
+    uint32_t parts, part_turns;
+    const bf16d_row_stats *stats;
+    const float *grad_logp, *grad_entropy;
+};
+hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream_t stream);
+
+// ---- policy loss ----------------------------------------------------------------
+constexpr uint32_t kPolicyGrid = 256;
+constexpr uint32_t kPolicySums = 5;   // loss, weight, kl, clipped, entropy
+struct PolicyArgs {
+    const float *logp, *old, *advantages, *weights, *ref, *entropy;
+    float *grad_logp, *grad_entropy;
+    uint64_t n;
+    double low, high;              // clip range of the ratio
+    double log_low, log_high;      // and of its logarithm
+    double kl_coef, entropy_coef, scale;
+    bf16d_policy_result *result;
+    uint64_t *partial;             // kPolicySums words a workgroup
+    uint32_t *done;
+};
+hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream);
+
+// ---- balance loss ------------------------------------------------------------------
+constexpr uint32_t kBalanceGrid = 256;
+struct BalanceArgs {
+    const void *logits, *chosen;
+    const uint8_t *mask;
+    uint64_t logits_stride, chosen_stride;
+    uint32_t rows, experts, choices, chosen_i32;
+    double balance_coef, z_coef;
+    int64_t *counts;
+    bf16d_balance_result *result;
+    uint64_t *sums;      // kBalanceWords accumulators, zero between calls
+    uint64_t *partial;   // a workgroup's sum of squares
+    uint32_t *done;
+};
+hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream);
+
+struct BalanceGradArgs {
+    const void *logits;
+    void *out;
+    const uint8_t *mask;
+    uint64_t logits_stride, out_stride;
+    uint32_t rows, experts;
+    double balance_coef, z_coef, scale;
+    const int64_t *counts, *tokens;
+    const bf16d_balance_result *result;
+};
+hipError_t launch_balance_backward(const BalanceGradArgs &a, bool f32, hipStream_t stream);
+
+// ---- device helpers -----------------------------------------------------------------
+typedef uint32_t word4 __attribute__((ext_vector_type(4)));
+// 16 bytes at an address of a 2- or 4-byte type's alignment
+typedef word4 word4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ const uint8_t *row_ptr(const RowSet &s, uint32_t row, uint32_t inner,
+                                                  uint32_t size) {
+    const uint32_t o = row / inner, i = row - o * inner;
+    return static_cast<const uint8_t *>(s.data) +
+           (o * s.outer_stride + i * s.inner_stride) * size;
+}
+__device__ __forceinline__ int64_t load_id(const uint8_t *p, uint32_t i32) {
+    return i32 ? (int64_t)*(const int32_t *)p : *(const int64_t *)p;
+}
+
+// Whether this is the last of `count` workgroups that call it on one counter
+// (as last_workgroup, whose count is the grid's).
+__device__ __forceinline__ bool last_of(uint32_t *done, uint32_t count, uint64_t dep) {
+    __shared__ bool s_last;
+    asm volatile("" ::"v"(dep) : "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 count - 1;
+    __syncthreads();
+    return s_last;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+    return v;
+}
+
+// the sum over the workgroup, in a fixed order; every thread gets it
+__device__ __forceinline__ double group_total(double v, double *s_tmp) {
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) s_tmp[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) t += s_tmp[w];
+    __syncthreads();
+    return t;
+}
+
+// Element k (known at compile time) of a vector of logits.
+template <bool kF32>
+__device__ __forceinline__ float element(const word4 &w, int k) {
+    if constexpr (kF32) return __uint_as_float(w[k]);
+    else return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+}
+
+}  // namespace bf16d

@@ -49,24 +49,6 @@ int upload(void *table, const std::vector<uint8_t> &host, hipStream_t stream) {
     return hipStreamSynchronize(stream) == hipSuccess ? BF16D_OK : BF16D_EHIP;
 }
 
-bool device_of(hipStream_t stream, int32_t &out) {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess) return false;
-    out = dev;
-    return true;
-}
-
-// BF16D_OK if `stream` belongs to the current device
-int stream_on_current(hipStream_t stream, int32_t &dev) {
-    if (!device_of(stream, dev)) return BF16D_EHIP;
-    if (stream) {
-        hipDevice_t sdev = -1;
-        if (hipStreamGetDevice(stream, &sdev) != hipSuccess) return BF16D_EHIP;
-        if (sdev != dev) return BF16D_EINVAL;
-    }
-    return BF16D_OK;
-}
-
 // a prepare waits for its upload, which a capture does not allow
 int prepare_stream(hipStream_t stream, int32_t &dev) {
     const int rc = stream_on_current(stream, dev);
@@ -74,10 +56,6 @@ int prepare_stream(hipStream_t stream, int32_t &dev) {
     hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &st) != hipSuccess) return BF16D_EHIP;
     return st == hipStreamCaptureStatusNone ? BF16D_OK : BF16D_EINVAL;
-}
-
-void add_range(std::vector<Range> &v, const void *p, uint64_t bytes, bool written) {
-    v.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
 }
 
 int norm_prepare(const bf16d_grad *grads, uint32_t count, void *table, size_t table_bytes,

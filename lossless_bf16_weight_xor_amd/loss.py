@@ -1,0 +1,370 @@
+"""The losses of a policy update (bf16delta_loss.h): log probabilities of given
+tokens with entropy and top alternatives, the clipped policy loss, the gradient
+of the logits, and a router's balance loss.  Argument marshalling only; the
+gradients go on through the model to GradNormBatch and AdamWBatch.
+
+    probs = TokenLogProbs(rows, vocab, entropy=True)
+    loss = PolicyLoss(rows)
+    probs.run(logits, tokens)
+    loss.run(probs.logp, old_logp, advantages, weights=weights, entropy=probs.entropy,
+             entropy_coef=1e-3, scale=1 / tokens_of_the_batch)
+    probs.backward(logits, tokens, loss.grad_logp, out=logits, grad_entropy=loss.grad_entropy)
+    ...                                   # logits hold their gradient
+
+Every call enqueues one kernel on the current stream and nothing else, and may be
+captured into a graph (keep the object and the tensors alive as long as it).  Results
+stay on the device, in buffers of the object that its next run overwrites.  Calls
+of one object must not overlap in time, nor replays of graphs that hold them.
+Tensors that are passed in stay their owner's, as in any torch call.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _native
+from . import _check_rc
+from .step import _raw_stream
+
+_LOGITS = {torch.bfloat16: _native.LOGITS_BF16, torch.float32: _native.LOGITS_F32}
+_IDS = {torch.int64: _native.IDS_I64, torch.int32: _native.IDS_I32}
+_BYTES = (torch.bool, torch.uint8)
+_MAX_ROWS = (1 << 24) - 1
+
+
+def _refuse(t, what: str, dtypes, shape, device) -> None:
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{what} must be a tensor on a HIP device (got "
+                        f"{getattr(t, 'device', type(t))}); there is no CPU path")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be of type {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{what}: the elements of a row must be adjacent")
+
+
+def _table(t, what: str, dtypes, device, width: int | None) -> None:
+    """A tensor of rows of `width` adjacent elements (None: of any width)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index
+            and t.dtype in dtypes):
+        _refuse(t, what, dtypes, None, device)
+    if t.dim() < 1 or (width is not None and t.shape[-1] != width):
+        raise ValueError(f"{what} must have rows of {width} elements, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+        _refuse(t, what, dtypes, None, device)
+
+
+def _row(t, what: str, dtypes, n: int, device) -> int:
+    """The address of n adjacent elements."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index
+            and t.dtype in dtypes):
+        _refuse(t, what, dtypes, None, device)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must hold {n} elements, contiguous; got {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _two_levels(t: torch.Tensor, dims: int) -> tuple[int, int]:
+    """The strides of a tensor's first `dims` dimensions (1 or 2), outer and inner."""
+    return (0, t.stride(0)) if dims == 1 else (t.stride(0), t.stride(1))
+
+
+class _Op:
+    """Buffers on one device, and calls on its current stream."""
+
+    def __init__(self, rows: int, device):
+        if not 0 <= int(rows) <= _MAX_ROWS:
+            raise ValueError(f"rows must be from 0 to {_MAX_ROWS}, got {rows}")
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise TypeError(f"a HIP device is needed, got {device}; there is no CPU path")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.rows = int(rows)
+        self.device = device
+        self._index = device.index
+        self._lib = _native.lib()
+        self._buffers = []
+        with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("prepare the operator before the capture: its workspace has "
+                                   "to be cleared once")
+            self._stream0 = _raw_stream(device.index)
+
+    def _zeros(self, size, dtype) -> torch.Tensor:
+        t = torch.zeros(size, dtype=dtype, device=self.device)
+        self._buffers.append(t)
+        return t
+
+    def _ready(self) -> None:
+        """The buffers are cleared, for any stream."""
+        with torch.cuda.device(self.device):
+            torch.cuda.current_stream().synchronize()
+
+    def _count(self, n: int) -> int:
+        if n > self.rows:
+            raise ValueError(f"{n} rows, but the operator was prepared for {self.rows}")
+        return n
+
+    def _hold(self, stream: int) -> None:
+        """Tells the allocator that another stream than the buffers' own works on them
+        (not in a capture: a graph needs the object alive anyway)."""
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                s = torch.cuda.current_stream()
+                for t in self._buffers:
+                    t.record_stream(s)
+
+    def _call(self, fn, what: str, *args) -> None:
+        """fn(*args, stream) on the current stream of the operator's device."""
+        stream = _raw_stream(self._index)
+        if stream != self._stream0:
+            self._hold(stream)
+        if torch.cuda.current_device() == self._index:
+            rc = fn(*args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, stream)
+        _check_rc(rc, what)
+
+
+class TokenLogProbs(_Op):
+    """Log probabilities of given tokens, with the distributions' entropy and the top
+    alternatives, and the gradient of the logits (bf16d_logprob,
+    bf16d_logprob_backward; special rows are described in bf16delta_loss.h).
+
+    rows    : the most rows (tokens) of a call
+    vocab   : logits of a row
+    entropy : whether the entropy is computed, too
+    top     : how many alternatives, at most 64
+
+    After a run over n rows, the first n entries of
+      logp     : float32, ln p of the given token; 0 where it is negative (a row
+                 that is left out)
+      entropy  : float32 (None without)
+      top_ids  : int64 (rows, top), the largest logits' ids, largest first, equal
+                 ones by their id; -1 where there are no more
+      top_logp : float32 (rows, top)
+    are its results, flat in the order of the rows; what is behind them is left as it
+    was."""
+
+    def __init__(self, rows: int, vocab: int, device=None, entropy: bool = False, top: int = 0):
+        if not 1 <= vocab <= _native.MAX_VOCAB:
+            raise ValueError(f"vocab must be from 1 to {_native.MAX_VOCAB}, got {vocab}")
+        if not 0 <= top <= _native.MAX_TOP:
+            raise ValueError(f"top must be from 0 to {_native.MAX_TOP}, got {top}")
+        super().__init__(rows, device)
+        self.vocab, self.top = int(vocab), int(top)
+        self.logp = self._zeros(self.rows, torch.float32)
+        self.entropy = self._zeros(self.rows, torch.float32) if entropy else None
+        self.stats = self._zeros((self.rows, 4), torch.float32)
+        self.top_ids = self._zeros((self.rows, self.top), torch.int64) if top else None
+        self.top_logp = self._zeros((self.rows, self.top), torch.float32) if top else None
+        size = int(self._lib.bf16d_logprob_workspace_bytes(self.rows, self.vocab, self.top))
+        self._workspace = self._zeros(size, torch.uint8)
+        self._ready()
+        self._ran = None    # rows of the last run
+        at = lambda t: t.data_ptr() if t is not None else None
+        self._job = _native.LogprobJob(vocab=self.vocab, top=self.top, logp=at(self.logp),
+                                       entropy=at(self.entropy), stats=at(self.stats),
+                                       top_ids=at(self.top_ids), top_logp=at(self.top_logp))
+        self._args = (ctypes.byref(self._job), self._workspace.data_ptr(), size)
+        self._grad_job = _native.LogprobGradJob(vocab=self.vocab, stats=self.stats.data_ptr())
+        self._grad_args = (ctypes.byref(self._grad_job),)
+
+    def _rows_of(self, job, logits, tokens) -> int:
+        """Fills in the logits and tokens of a call and returns its number of rows."""
+        _table(logits, "logits", _LOGITS, self.device, self.vocab)
+        dims = logits.dim() - 1
+        if dims not in (1, 2):
+            raise ValueError(f"logits must be (rows, vocab) or (batch, length, vocab), got "
+                             f"{tuple(logits.shape)}")
+        if not (isinstance(tokens, torch.Tensor) and tokens.is_cuda
+                and tokens.get_device() == self._index and tokens.dtype in _IDS
+                and tokens.shape == logits.shape[:-1]):
+            _refuse(tokens, "tokens", _IDS, logits.shape[:-1], self.device)
+        job.outer, job.inner = (1, logits.shape[0]) if dims == 1 else logits.shape[:2]
+        job.logits = logits.data_ptr()
+        job.logits_outer, job.logits_inner = _two_levels(logits, dims)
+        job.tokens = tokens.data_ptr()
+        job.tokens_outer, job.tokens_inner = _two_levels(tokens, dims)
+        job.logits_dtype, job.token_dtype = _LOGITS[logits.dtype], _IDS[tokens.dtype]
+        return self._count(job.outer * job.inner)
+
+    def run(self, logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0) -> None:
+        """logits: bf16 or fp32, (rows, vocab) or (batch, length, vocab), a row's
+        elements adjacent, any strides else.  tokens: int64 or int32, one id a row (a
+        negative one leaves the row out).  temperature: what the logits are divided
+        by, from 2^-20 to 2^20."""
+        if not 2.0 ** -20 <= temperature <= 2.0 ** 20:
+            raise ValueError(f"temperature must be from 2^-20 to 2^20, got {temperature}")
+        n = self._rows_of(self._job, logits, tokens)
+        self._job.temperature = temperature
+        self._call(self._lib.bf16d_logprob, "bf16d_logprob", *self._args)
+        self._ran = n
+
+    def backward(self, logits: torch.Tensor, tokens: torch.Tensor, grad_logp: torch.Tensor,
+                 out: torch.Tensor, grad_entropy: torch.Tensor | None = None) -> None:
+        """The gradient of sum(grad_logp * logp + grad_entropy * entropy) by the logits, into
+        `out` (their type and shape; the logits themselves are fine).  logits and
+        tokens: those of the last run; grad_logp, grad_entropy: float32, one a row."""
+        job = self._grad_job
+        n = self._rows_of(job, logits, tokens)
+        if n != self._ran:
+            raise ValueError(f"{n} rows, but the last run had {self._ran}: backward needs its "
+                             f"softmax sums")
+        _table(out, "out", (logits.dtype,), self.device, self.vocab)
+        if out.shape != logits.shape:
+            raise ValueError(f"out must have the logits' shape {tuple(logits.shape)}, got "
+                             f"{tuple(out.shape)}")
+        job.out = out.data_ptr()
+        job.out_outer, job.out_inner = _two_levels(out, logits.dim() - 1)
+        job.grad_logp = _row(grad_logp, "grad_logp", (torch.float32,), n, self.device)
+        job.grad_entropy = None
+        if grad_entropy is not None:
+            if self.entropy is None:
+                raise ValueError("grad_entropy needs an operator prepared with entropy=True")
+            job.grad_entropy = _row(grad_entropy, "grad_entropy", (torch.float32,), n, self.device)
+        self._call(self._lib.bf16d_logprob_backward, "bf16d_logprob_backward", *self._grad_args)
+
+
+class PolicyLoss(_Op):
+    """The clipped policy loss of up to `rows` tokens and its gradients
+    (bf16d_policy_loss; the formulas are in bf16delta_loss.h).
+
+    After a run over n tokens, on the device:
+      grad_logp, grad_entropy : float32, their first n entries
+      loss    : scale * the weighted sum of the tokens' losses
+      weight  : the sum of the weights
+      kl, clipped, entropy : weighted means, of r - 1 - ln r, of the tokens whose
+                ratio was clipped, and of the entropies
+    the last five as 0-dim float32 views of one small buffer."""
+
+    def __init__(self, rows: int, device=None):
+        super().__init__(rows, device)
+        self.grad_logp = self._zeros(self.rows, torch.float32)
+        self.grad_entropy = self._zeros(self.rows, torch.float32)
+        self.result = self._zeros(8, torch.float32)
+        self.loss, self.weight, self.kl, self.clipped, self.entropy = self.result[:5].unbind()
+        size = int(self._lib.bf16d_policy_loss_workspace_bytes())
+        self._workspace = self._zeros(size, torch.uint8)
+        self._ready()
+        self._job = _native.PolicyJob(grad_logp=self.grad_logp.data_ptr())
+        self._args = (ctypes.byref(self._job), self.result.data_ptr(),
+                      self._workspace.data_ptr(), size)
+
+    def run(self, logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+            weights: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None,
+            entropy: torch.Tensor | None = None, clip: tuple[float, float] = (0.2, 0.2),
+            kl_coef: float = 0.0, entropy_coef: float = 0.0, scale: float = 1.0) -> None:
+        """All tensors: float32, contiguous, one number a token.
+
+        logp, old_logp : under the policy, and under the one that drew the tokens
+        weights  : of the tokens (0: left out, whatever its numbers are); None: all 1
+        ref_logp : under the reference policy, for kl_coef
+        entropy  : of the policy, for entropy_coef and the mean
+        clip     : how far a ratio counts below and above 1 (infinity above: no bound)
+        scale    : of the loss and the gradients, 1 / the batch's tokens for example"""
+        job, f32 = self._job, (torch.float32,)
+        n = self._count(logp.numel() if isinstance(logp, torch.Tensor) else 0)
+        job.n = n
+        job.logp = _row(logp, "logp", f32, n, self.device)
+        job.old = _row(old_logp, "old_logp", f32, n, self.device)
+        job.advantages = _row(advantages, "advantages", f32, n, self.device)
+        job.weights = None if weights is None else _row(weights, "weights", f32, n, self.device)
+        job.ref = None if ref_logp is None else _row(ref_logp, "ref_logp", f32, n, self.device)
+        job.entropy = job.grad_entropy = None
+        if entropy is not None:
+            job.entropy = _row(entropy, "entropy", f32, n, self.device)
+            job.grad_entropy = self.grad_entropy.data_ptr()
+        if (kl_coef != 0.0 and ref_logp is None) or (entropy_coef != 0.0 and entropy is None):
+            raise ValueError("kl_coef needs ref_logp, and entropy_coef needs entropy")
+        job.clip_low, job.clip_high = clip
+        job.kl_coef, job.entropy_coef, job.scale = kl_coef, entropy_coef, scale
+        self._call(self._lib.bf16d_policy_loss, "bf16d_policy_loss", *self._args)
+
+
+class RouterBalance(_Op):
+    """The balance loss of a router over `experts`, how often each was chosen, and the
+    gradient of the router's logits (bf16d_balance, bf16d_balance_backward; the
+    formulas are in bf16delta_loss.h), for up to `rows` tokens a call.
+
+    After a run, on the device:
+      counts  : int64, one number an expert
+      tokens  : int64, the tokens that count
+      loss    : balance_coef * balance + z_coef * z, NaN where an id is out of range
+      balance : 1 where the choices or the probabilities are even
+      z       : the mean square of ln sum e^x
+    the last four as 0-dim views of one small buffer.
+
+    Where several ranks hold a part of the batch each, all-reduce counts and tokens
+    (sum) between run and backward: the gradients are then those of the whole
+    batch's loss."""
+
+    def __init__(self, rows: int, experts: int, device=None, balance_coef: float = 0.01,
+                 z_coef: float = 0.0):
+        if not 1 <= experts <= _native.MAX_EXPERTS:
+            raise ValueError(f"experts must be from 1 to {_native.MAX_EXPERTS}, got {experts}")
+        super().__init__(rows, device)
+        self.experts = int(experts)
+        self.counts = self._zeros(self.experts, torch.int64)
+        self.result = self._zeros(4, torch.int64)
+        self.loss, self.balance, self.z = self.result.view(torch.float32)[:3].unbind()
+        self.tokens = self.result[2]
+        size = int(self._lib.bf16d_balance_workspace_bytes(self.experts))
+        self._workspace = self._zeros(size, torch.uint8)
+        self._ready()
+        self._ran = False
+        coefs = dict(balance_coef=balance_coef, z_coef=z_coef)
+        self._job = _native.BalanceJob(experts=self.experts, counts=self.counts.data_ptr(), **coefs)
+        self._args = (ctypes.byref(self._job), self.result.data_ptr(),
+                      self._workspace.data_ptr(), size)
+        self._grad_job = _native.BalanceGradJob(
+            experts=self.experts, counts=self.counts.data_ptr(), tokens=self.tokens.data_ptr(),
+            result=self.result.data_ptr(), **coefs)
+        self._grad_args = (ctypes.byref(self._grad_job),)
+
+    def _rows_of(self, job, logits, mask) -> int:
+        _table(logits, "logits", _LOGITS, self.device, self.experts)
+        if logits.dim() != 2:
+            raise ValueError(f"logits must be (tokens, experts), got {tuple(logits.shape)}")
+        n = self._count(logits.shape[0])
+        job.rows, job.logits, job.logits_stride = n, logits.data_ptr(), logits.stride(0)
+        job.logits_dtype = _LOGITS[logits.dtype]
+        job.mask = None if mask is None else _row(mask, "mask", _BYTES, n, self.device)
+        return n
+
+    def run(self, logits: torch.Tensor, chosen: torch.Tensor,
+            mask: torch.Tensor | None = None) -> None:
+        """logits: bf16 or fp32, (tokens, experts).  chosen: int64 or int32, (tokens,
+        choices), the ids of each token's experts (a negative one is no choice).
+        mask: bool or uint8, which tokens count; None: all."""
+        job = self._job
+        n = self._rows_of(job, logits, mask)
+        _table(chosen, "chosen", _IDS, self.device, None)
+        if chosen.dim() != 2 or chosen.shape[0] != n or not 1 <= chosen.shape[1] <= self.experts:
+            raise ValueError(f"chosen must be (tokens, choices) for {n} tokens and at most "
+                             f"{self.experts} choices, got {tuple(chosen.shape)}")
+        job.chosen, job.chosen_stride = chosen.data_ptr(), chosen.stride(0)
+        job.choices, job.chosen_dtype = chosen.shape[1], _IDS[chosen.dtype]
+        self._call(self._lib.bf16d_balance, "bf16d_balance", *self._args)
+        self._ran = True
+
+    def backward(self, logits: torch.Tensor, out: torch.Tensor, mask: torch.Tensor | None = None,
+                 scale: float = 1.0) -> None:
+        """scale * the gradient of the loss by the logits, into `out` (their type and shape;
+        the logits themselves are fine).  logits, mask: those of the last run."""
+        job = self._grad_job
+        if not self._ran:
+            raise ValueError("backward needs the counts of a run")
+        self._rows_of(job, logits, mask)
+        _table(out, "out", (logits.dtype,), self.device, self.experts)
+        if out.shape != logits.shape:
+            raise ValueError(f"out must have the logits' shape {tuple(logits.shape)}, got "
+                             f"{tuple(out.shape)}")
+        job.out, job.out_stride, job.scale = out.data_ptr(), out.stride(0), scale
+        self._call(self._lib.bf16d_balance_backward, "bf16d_balance_backward", *self._grad_args)
