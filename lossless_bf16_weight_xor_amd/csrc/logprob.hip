@@ -44,9 +44,9 @@ __device__ __forceinline__ void merge(Sums &a, Sums b, float c) {
 }
 // the sums of the whole workgroup, in every thread
 __device__ __forceinline__ Sums group_sums(Sums a, float c, float (*s_tmp)[3]) {
-    shift(a, wave_max(a.m), c);
-    a.s = wave_sum(a.s);
-    a.w = wave_sum(a.w);
+    shift(a, lanes_reduce<Max>(a.m), c);
+    a.s = lanes_reduce<Add>(a.s);
+    a.w = lanes_reduce<Add>(a.w);
     const uint32_t wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
         s_tmp[wave][0] = a.m;
@@ -138,45 +138,75 @@ __device__ __forceinline__ void insert(TopList &l, uint64_t key, uint32_t top) {
 }
 
 // ---- forward ---------------------------------------------------------------------------
-// the vector's elements from `count` on are no tokens
+// A row is cut into vectors at 16-byte addresses: vector i holds its elements from
+// i * kPer - skip on, skip being how many elements lie between such an address
+// and the row's start.  Only the first and the last vector can be partial.
+// (Vectors counted from the row's own start read 10 to 20 % slower where that is odd.)
 template <bool kF32>
-__device__ __forceinline__ word4 load_tail(const uint8_t *p, uint32_t count) {
-    constexpr uint32_t kSize = kF32 ? 4 : 2, kPer = 16 / kSize;
+struct RowVectors {
+    static constexpr uint32_t kPer = kF32 ? 4 : 8, kSize = kF32 ? 4 : 2;
+    const uint8_t *row;
+    uint32_t skip, vocab;
+
+    __device__ __forceinline__ RowVectors(const uint8_t *at, uint32_t n)
+        : row(at), skip(((uint32_t)(uintptr_t)at & 15u) / kSize), vocab(n) {}
+    // the id of vector i's first element (below 0 in a partial first one, as uint32_t)
+    __device__ __forceinline__ uint32_t first(uint32_t i) const { return i * kPer - skip; }
+    __device__ __forceinline__ const uint8_t *at(uint32_t i) const {
+        return row + (int64_t)(int32_t)first(i) * kSize;
+    }
+    __device__ __forceinline__ bool whole(uint32_t i) const {
+        return first(i) < vocab && vocab - first(i) >= kPer;
+    }
+    // whether every vector of the turn is
+    __device__ __forceinline__ bool whole_turn(uint32_t turn) const {
+        return (turn > 0 || skip == 0) && (turn + 1) * kTurnVectors * kPer <= vocab + skip;
+    }
+    __device__ __forceinline__ uint32_t turns() const {
+        return (vocab + skip + kTurnVectors * kPer - 1) / (kTurnVectors * kPer);
+    }
+};
+
+// what is no token is -infinity
+template <bool kF32>
+__device__ __forceinline__ word4 load_partial(const RowVectors<kF32> &r, uint32_t i) {
+    constexpr uint32_t kPer = RowVectors<kF32>::kPer;
+    const uint32_t first = r.first(i);
     word4 w;
     if constexpr (kF32) w = word4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u};
     else w = word4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
 #pragma unroll
     for (uint32_t k = 0; k < kPer; ++k) {
-        if (k >= count) continue;
+        if (first + k >= r.vocab) continue;
         if constexpr (kF32) {
-            w[k] = ((const uint32_t *)p)[k];
+            w[k] = ((const uint32_t *)r.row)[first + k];
         } else {
-            const uint32_t e = ((const uint16_t *)p)[k];
+            const uint32_t e = ((const uint16_t *)r.row)[first + k];
             w[k >> 1] = k & 1 ? (w[k >> 1] & 0xFFFFu) | e << 16 : (w[k >> 1] & 0xFFFF0000u) | e;
         }
     }
     return w;
 }
 
-// The thread's vectors of a turn (vector q * kThreads + threadIdx.x of it).
-template <bool kF32>
-__device__ __forceinline__ void load_turn(word4 (&v)[4], const uint8_t *row, uint32_t turn,
-                                          uint32_t vocab) {
-    constexpr uint32_t kPer = kF32 ? 4 : 8;
+// The thread's vectors of a turn (vector q * kThreads + threadIdx.x of it).  kKeep: they
+// may stay in the caches.
+template <bool kKeep, bool kF32>
+__device__ __forceinline__ void load_turn(word4 (&v)[4], const RowVectors<kF32> &r,
+                                          uint32_t turn) {
     const uint32_t first = turn * kTurnVectors + threadIdx.x;
-    const uint32_t full = vocab / kPer;
-    if ((turn + 1) * kTurnVectors <= full) {
+    if (r.whole_turn(turn)) {
+        const auto *p = (const word4 *)r.at(first);
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q)
-            v[q] = *(const word4_any *)(row + 16ull * (first + q * kThreads));
+        for (uint32_t q = 0; q < 4; ++q) {
+            if constexpr (kKeep) v[q] = p[q * kThreads];
+            else v[q] = __builtin_nontemporal_load(p + q * kThreads);
+        }
         return;
     }
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
         const uint32_t i = first + q * kThreads;
-        const uint8_t *p = row + 16ull * i;
-        if (i < full) v[q] = *(const word4_any *)p;
-        else v[q] = load_tail<kF32>(p, i == full ? vocab % kPer : 0);
+        v[q] = r.whole(i) ? *(const word4 *)r.at(i) : load_partial(r, i);
     }
 }
 
@@ -230,7 +260,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, uint32_t row, co
     }
 }
 
-template <bool kF32, bool kEntropy, bool kTop>
+template <bool kF32, bool kEntropy, bool kTop, bool kKeep>
 __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
     __shared__ float s_tmp[kWaves][3];
     __shared__ uint64_t s_list[kTop ? kWaves : 1][64];
@@ -249,14 +279,18 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
         else own = __uint_as_float((uint32_t)((const uint16_t *)x)[token] << 16);
     }
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t turns = (a.vocab + kTurnVectors * kPer - 1) / (kTurnVectors * kPer);
+    const RowVectors<kF32> r(x, a.vocab);
+    const uint32_t turns = r.turns();
     const uint32_t begin = part * a.part_turns;
     const uint32_t end = begin + a.part_turns < turns ? begin + a.part_turns : turns;
     Sums mine = {-INFINITY, 0.0f, 0.0f};
     TopList best = {0, 0, -INFINITY};
+    word4 v[4], next[4];
+    if (begin < end) load_turn<kKeep>(next, r, begin);
     for (uint32_t turn = begin; turn < end; ++turn) {
-        word4 v[4];
-        load_turn<kF32>(v, x, turn, a.vocab);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = next[q];
+        if (turn + 1 < end) load_turn<kKeep>(next, r, turn + 1);
         float m = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -273,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
                         const float e = element<kF32>(v[q], k);
                         if (!__ballot(e >= best.least)) continue;
                         const uint32_t id =
-                            (turn * kTurnVectors + q * kThreads + threadIdx.x) * kPer + k;
+                            r.first(turn * kTurnVectors + q * kThreads + threadIdx.x) + k;
                         insert(best, e >= best.least ? key_of(e, id) : 0, a.top);
                     }
             }
@@ -334,33 +368,26 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
 }
 
 // ---- backward ------------------------------------------------------------------------------
+// The vectors of a turn, as they were loaded, into another row.
 template <bool kF32>
-__device__ __forceinline__ void store_turn(const word4 (&v)[4], uint8_t *row, uint32_t turn,
-                                           uint32_t vocab) {
-    constexpr uint32_t kPer = kF32 ? 4 : 8;
-    const uint32_t first = turn * kTurnVectors + threadIdx.x;
-    const uint32_t full = vocab / kPer;
+__device__ __forceinline__ void store_turn(const word4 (&v)[4], uint8_t *out,
+                                           const RowVectors<kF32> &r, uint32_t turn) {
+    constexpr uint32_t kPer = RowVectors<kF32>::kPer, kSize = RowVectors<kF32>::kSize;
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-        const uint32_t i = first + q * kThreads;
-        uint8_t *p = row + 16ull * i;
-        if (i < full) {
-            *(word4_any *)p = v[q];
-        } else if (i == full) {
+        const uint32_t i = turn * kTurnVectors + threadIdx.x + q * kThreads;
+        const uint32_t first = r.first(i);
+        if (r.whole(i)) {
+            __builtin_nontemporal_store(v[q], (word4_any *)(out + (uint64_t)first * kSize));
+        } else {
 #pragma unroll
             for (uint32_t k = 0; k < kPer; ++k) {
-                if (k >= vocab % kPer) continue;
-                if constexpr (kF32) ((uint32_t *)p)[k] = v[q][k];
-                else ((uint16_t *)p)[k] = (uint16_t)(v[q][k >> 1] >> (16 * (k & 1)));
+                if (first + k >= r.vocab) continue;
+                if constexpr (kF32) ((uint32_t *)out)[first + k] = v[q][k];
+                else ((uint16_t *)out)[first + k] = (uint16_t)(v[q][k >> 1] >> (16 * (k & 1)));
             }
         }
     }
-}
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // One part of a row.  g_j = -p_j (A + B t_j) with t_j = log2 p_j, A = (a + h H) / T
@@ -372,7 +399,8 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
     const int64_t token =
         load_id(row_ptr(g.tokens, row, g.inner, g.token_i32 ? 4 : 8), g.token_i32);
     uint8_t *out = const_cast<uint8_t *>(row_ptr(g.out, row, g.inner, kSize));
-    const uint32_t turns = (g.vocab + kTurnVectors * kPer - 1) / (kTurnVectors * kPer);
+    const RowVectors<kF32> r(row_ptr(g.logits, row, g.inner, kSize), g.vocab);
+    const uint32_t turns = r.turns();
     const uint32_t begin = part * g.part_turns;
     const uint32_t end = begin + g.part_turns < turns ? begin + g.part_turns : turns;
     const float a = g.grad_logp[row], h = kEntropy ? g.grad_entropy[row] : 0.0f;
@@ -383,54 +411,56 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
         const uint32_t fill = zero ? 0u : kF32 ? 0x7FC00000u : 0x7FC07FC0u;
         const word4 v[4] = {word4{fill, fill, fill, fill}, word4{fill, fill, fill, fill},
                             word4{fill, fill, fill, fill}, word4{fill, fill, fill, fill}};
-        for (uint32_t turn = begin; turn < end; ++turn) store_turn<kF32>(v, out, turn, g.vocab);
+        for (uint32_t turn = begin; turn < end; ++turn) store_turn(v, out, r, turn);
         return;
     }
-    const uint8_t *x = row_ptr(g.logits, row, g.inner, kSize);
     const float inv_t = s.scale * kLn2;
     const float add = a * inv_t;
     const float A = kEntropy ? -(a + h * s.entropy) * inv_t : -add;
     const float B = -h * inv_t * kLn2;
     for (uint32_t turn = begin; turn < end; ++turn) {
         word4 v[4];
-        load_turn<kF32>(v, x, turn, g.vocab);
+        load_turn<false>(v, r, turn);
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q) {
-            const uint32_t id = (turn * kTurnVectors + q * kThreads + threadIdx.x) * kPer;
+            const uint32_t id = r.first(turn * kTurnVectors + q * kThreads + threadIdx.x);
             const uint32_t hit = (uint32_t)token - id;   // below kPer: the token is here
-            float r[kPer];
+            float d[kPer];
 #pragma unroll
             for (uint32_t k = 0; k < kPer; ++k) {
                 const float t = (element<kF32>(v[q], k) - s.max) * s.scale - s.log2_sum;
                 const float p = exp2_fast(t);
-                r[k] = kEntropy ? p * (A + B * fmaxf(t, kNone)) : p * A;
-                if (k == hit) r[k] += add;
+                d[k] = kEntropy ? p * (A + B * fmaxf(t, kNone)) : p * A;
+                if (k == hit) d[k] += add;
             }
             if constexpr (kF32) {
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) v[q][k] = __float_as_uint(r[k]);
+                for (uint32_t k = 0; k < 4; ++k) v[q][k] = __float_as_uint(d[k]);
             } else {
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) v[q][k] = pack_bf16(r[2 * k], r[2 * k + 1]);
+                for (uint32_t k = 0; k < 4; ++k) v[q][k] = pack_bf16(d[2 * k], d[2 * k + 1]);
             }
         }
-        store_turn<kF32>(v, out, turn, g.vocab);
+        store_turn(v, out, r, turn);
     }
 }
 
-template <bool kF32>
-hipError_t launch_typed(const LogprobArgs &a, hipStream_t stream) {
-    auto *kernel = a.entropy ? (a.top ? logprob_kernel<kF32, true, true>
-                                      : logprob_kernel<kF32, true, false>)
-                             : (a.top ? logprob_kernel<kF32, false, true>
-                                      : logprob_kernel<kF32, false, false>);
+template <bool kF32, bool kEntropy>
+hipError_t launch_forward(const LogprobArgs &a, bool keep, hipStream_t stream) {
+    // few rows have alternatives: they stay in the caches in any case
+    auto *kernel = a.top  ? logprob_kernel<kF32, kEntropy, true, true>
+                   : keep ? logprob_kernel<kF32, kEntropy, false, true>
+                          : logprob_kernel<kF32, kEntropy, false, false>;
     return launch_one(kernel, a.rows * a.parts, kThreads, a, 0, stream);
 }
-
 }  // namespace
 
-hipError_t launch_logprob(const LogprobArgs &a, bool f32, hipStream_t stream) {
-    return f32 ? launch_typed<true>(a, stream) : launch_typed<false>(a, stream);
+hipError_t launch_logprob(const LogprobArgs &a, bool f32, bool keep, hipStream_t stream) {
+    if (f32)
+        return a.entropy ? launch_forward<true, true>(a, keep, stream)
+                         : launch_forward<true, false>(a, keep, stream);
+    return a.entropy ? launch_forward<false, true>(a, keep, stream)
+                     : launch_forward<false, false>(a, keep, stream);
 }
 
 hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream_t stream) {

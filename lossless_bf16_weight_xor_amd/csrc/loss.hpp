@@ -17,10 +17,14 @@ namespace bf16d {
 constexpr uint32_t kTurnVectors = 4 * kThreads;
 constexpr uint32_t kLogprobGroups = 1024;
 constexpr uint32_t vector_elems(uint32_t dtype) { return dtype == BF16D_LOGITS_F32 ? 4 : 8; }
-inline uint32_t turns_of(uint32_t vocab, uint32_t dtype) {
+// The most turns of a row; aligned: all rows start at 16-byte addresses.
+inline uint32_t turns_of(uint32_t vocab, uint32_t dtype, bool aligned) {
     const uint32_t per = kTurnVectors * vector_elems(dtype);
-    return (vocab + per - 1) / per;
+    return (vocab + (aligned ? 0 : vector_elems(dtype) - 1) + per - 1) / per;
 }
+// Logits of up to this many bytes are left in the last-level cache for the
+// backward pass.
+constexpr uint64_t kLogprobKept = 128u << 20;
 
 // Rows of a call, as the device sees them.
 struct RowSet {
@@ -41,7 +45,8 @@ struct LogprobArgs {
     uint64_t *partial;   // (2 + top) words of each part of each row
     uint32_t *done;      // of each row
 };
-hipError_t launch_logprob(const LogprobArgs &a, bool f32, hipStream_t stream);
+// keep: the logits may stay in the caches
+hipError_t launch_logprob(const LogprobArgs &a, bool f32, bool keep, hipStream_t stream);
 
 struct LogprobGradArgs {
     RowSet logits, tokens, out;
@@ -54,6 +59,7 @@ hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream
 
 // ---- policy loss ----------------------------------------------------------------
 constexpr uint32_t kPolicyGrid = 256;
+constexpr uint32_t kPolicyThreads = 1024;
 constexpr uint32_t kPolicySums = 5;   // loss, weight, kl, clipped, entropy
 struct PolicyArgs {
     const float *logp, *old, *advantages, *weights, *ref, *entropy;
@@ -69,7 +75,11 @@ struct PolicyArgs {
 hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream);
 
 // ---- balance loss ------------------------------------------------------------------
+// A workgroup of 16 waves for each CU: as many rows in flight as with small
+// ones, and fewer additions to the shared sums at the end.
 constexpr uint32_t kBalanceGrid = 256;
+constexpr uint32_t kBalanceThreads = 1024;
+constexpr uint32_t kBalanceGradGrid = 2048;   // of four waves
 struct BalanceArgs {
     const void *logits, *chosen;
     const uint8_t *mask;
@@ -124,20 +134,76 @@ __device__ __forceinline__ bool last_of(uint32_t *done, uint32_t count, uint64_t
     return s_last;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+// ---- reductions over the lanes of a wave ------------------------------------------
+// v combined with the value of another lane, step by step, over groups of `lanes`
+// (a power of two, the same in the whole wave) neighbouring lanes, all of which
+// get the result.  DPP moves and lane swaps take a few cycles where a shuffle
+// through LDS takes a hundred.  The order is fixed.
+struct Add {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+template <int kCtrl>
+__device__ __forceinline__ float dpp_value(float v) {
+    return __uint_as_float(dpp_src<kCtrl>(__float_as_uint(v)));
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp_value(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)dpp_src<kCtrl>((uint32_t)(b >> 32)) << 32 |
+                                            dpp_src<kCtrl>((uint32_t)b)));
+}
+// (v of the even 16- or 32-lane half in both halves, v of the odd one in both)
+template <int kHalf>
+__device__ __forceinline__ void both_halves(float v, float &even, float &odd) {
+    const uint32_t b = __float_as_uint(v);
+    auto r = kHalf == 16 ? __builtin_amdgcn_permlane16_swap(b, b, false, false)
+                         : __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    even = __uint_as_float(r[0]);
+    odd = __uint_as_float(r[1]);
+}
+template <int kHalf>
+__device__ __forceinline__ void both_halves(double v, double &even, double &odd) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t l = (uint32_t)b, h = (uint32_t)(b >> 32);
+    auto lo = kHalf == 16 ? __builtin_amdgcn_permlane16_swap(l, l, false, false)
+                          : __builtin_amdgcn_permlane32_swap(l, l, false, false);
+    auto hi = kHalf == 16 ? __builtin_amdgcn_permlane16_swap(h, h, false, false)
+                          : __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    even = __longlong_as_double((long long)((uint64_t)hi[0] << 32 | lo[0]));
+    odd = __longlong_as_double((long long)((uint64_t)hi[1] << 32 | lo[1]));
+}
+template <typename Op, typename T>
+__device__ __forceinline__ T lanes_reduce(T v, uint32_t lanes = 64) {
+    const Op op;
+    T even, odd;
+    if (lanes > 1) v = op(v, dpp_value<0xB1>(v));     // quad_perm 1 0 3 2
+    if (lanes > 2) v = op(v, dpp_value<0x4E>(v));     // quad_perm 2 3 0 1
+    if (lanes > 4) v = op(v, dpp_value<0x141>(v));    // row_half_mirror
+    if (lanes > 8) v = op(v, dpp_value<0x140>(v));    // row_mirror
+    if (lanes > 16) {
+        both_halves<16>(v, even, odd);
+        v = op(even, odd);
+    }
+    if (lanes > 32) {
+        both_halves<32>(v, even, odd);
+        v = op(even, odd);
+    }
     return v;
 }
 
-// the sum over the workgroup, in a fixed order; every thread gets it
-__device__ __forceinline__ double group_total(double v, double *s_tmp) {
-    v = wave_sum(v);
+// the sum over a workgroup of kCount waves, in a fixed order; every thread gets it
+template <uint32_t kCount>
+__device__ __forceinline__ double group_total(double v, double (&s_tmp)[kCount]) {
+    v = lanes_reduce<Add>(v);
     if ((threadIdx.x & 63) == 0) s_tmp[threadIdx.x >> 6] = v;
     __syncthreads();
     double t = 0.0;
 #pragma unroll
-    for (uint32_t w = 0; w < kWaves; ++w) t += s_tmp[w];
+    for (uint32_t w = 0; w < kCount; ++w) t += s_tmp[w];
     __syncthreads();
     return t;
 }
@@ -147,6 +213,13 @@ template <bool kF32>
 __device__ __forceinline__ float element(const word4 &w, int k) {
     if constexpr (kF32) return __uint_as_float(w[k]);
     else return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+}
+
+// two floats to bf16, nearest even
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef float pair __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair{lo, hi}, bf16_pair));
 }
 
 }  // namespace bf16d

@@ -46,6 +46,12 @@ bool rows_apart(const bf16d_rows &r, uint64_t outer, uint64_t inner, uint64_t wi
            nested(outer, r.outer_stride, inner, r.inner_stride);
 }
 
+// whether every row starts at a 16-byte address
+bool rows_aligned(const bf16d_rows &r, uint64_t outer, uint64_t inner, uint64_t size) {
+    return aligned16(r.data) && (outer <= 1 || r.outer_stride * size % 16 == 0) &&
+           (inner <= 1 || r.inner_stride * size % 16 == 0);
+}
+
 RowSet row_set(const bf16d_rows &r) { return RowSet{r.data, r.outer_stride, r.inner_stride}; }
 
 // rows = outer * inner; false where there are too many
@@ -90,16 +96,17 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
         !aligned(J.logits.data, logits_size(J.logits_dtype)) ||
         !aligned(J.tokens.data, id_size(J.token_dtype)))
         return BF16D_EINVAL;
+    const uint64_t size = logits_size(J.logits_dtype);
+    const uint32_t turns = turns_of(J.vocab, J.logits_dtype,
+                                    rows_aligned(J.logits, J.outer, J.inner, size));
     if (rows > 0) {
         if (!J.logits.data || !J.tokens.data || !J.logp) return BF16D_EINVAL;
         if ((J.top > 0) != (J.top_ids != nullptr) || (J.top > 0) != (J.top_logp != nullptr))
             return BF16D_EINVAL;
         uint64_t logits_bytes = 0, token_bytes = 0;
-        if (!extent(J.logits, J.outer, J.inner, J.vocab, logits_size(J.logits_dtype),
-                    logits_bytes) ||
+        if (!extent(J.logits, J.outer, J.inner, J.vocab, size, logits_bytes) ||
             !extent(J.tokens, J.outer, J.inner, 1, id_size(J.token_dtype), token_bytes))
             return BF16D_EINVAL;
-        const uint32_t turns = turns_of(J.vocab, J.logits_dtype);
         const size_t need = logprob_workspace(rows, turns, J.top);
         if (workspace_bytes < need || (need && !workspace)) return BF16D_EINVAL;
         std::vector<Range> ranges;
@@ -116,7 +123,6 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     int32_t dev = -1;
     const int rc = stream_on_current(stream, dev);
     if (rc != BF16D_OK || rows == 0) return rc;
-    const uint32_t turns = turns_of(J.vocab, J.logits_dtype);
     LogprobArgs a{};
     a.logits = row_set(J.logits);
     a.tokens = row_set(J.tokens);
@@ -127,6 +133,7 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     a.top = J.top;
     a.parts = parts_of(rows, turns);
     a.part_turns = (turns + a.parts - 1) / a.parts;
+    const bool keep = J.stats && rows * J.vocab * size <= kLogprobKept;
     a.scale = float(1.4426950408889634 / J.temperature);
     a.inv_t = float(1.0 / J.temperature);
     a.logp = J.logp;
@@ -136,7 +143,7 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     a.top_logp = J.top_logp;
     a.done = static_cast<uint32_t *>(workspace);
     a.partial = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
-    return launch_logprob(a, J.logits_dtype == BF16D_LOGITS_F32, stream) == hipSuccess
+    return launch_logprob(a, J.logits_dtype == BF16D_LOGITS_F32, keep, stream) == hipSuccess
                ? BF16D_OK
                : BF16D_EHIP;
 }
@@ -179,7 +186,8 @@ int logprob_backward(const bf16d_logprob_grad_job *job, hipStream_t stream) {
     int32_t dev = -1;
     const int rc = stream_on_current(stream, dev);
     if (rc != BF16D_OK || rows == 0) return rc;
-    const uint32_t turns = turns_of(J.vocab, J.logits_dtype);
+    const uint32_t turns = turns_of(J.vocab, J.logits_dtype,
+                                    rows_aligned(J.logits, J.outer, J.inner, size));
     LogprobGradArgs a{};
     a.logits = row_set(J.logits);
     a.tokens = row_set(J.tokens);
@@ -397,8 +405,8 @@ extern "C" {
 size_t bf16d_logprob_workspace_bytes(uint64_t rows, uint32_t vocab, uint32_t top) {
     if (vocab == 0) return 0;
     // fp32 rows have more turns
-    return logprob_workspace(rows, turns_of(std::min(vocab, BF16D_MAX_VOCAB), BF16D_LOGITS_F32),
-                             std::min(top, BF16D_MAX_TOP));
+    const uint32_t turns = turns_of(std::min(vocab, BF16D_MAX_VOCAB), BF16D_LOGITS_F32, false);
+    return logprob_workspace(rows, turns, std::min(top, BF16D_MAX_TOP));
 }
 
 int bf16d_logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_bytes,
