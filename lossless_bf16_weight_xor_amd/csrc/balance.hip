@@ -13,61 +13,91 @@
 namespace bf16d {
 namespace {
 
-constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr double kFixed = 68719476736.0;   // 2^36: sums of p stay below 2^24 rows * 2^36
 
 // what the accumulators after the 2 * experts counts and sums are
 enum { kSumTokens = 0, kSumBadIds = 1, kSumBadRows = 2, kSumWords = 3 };
 
 // Which experts a lane holds: kVec pieces of kPer neighbours, piece v from
-// start[v] on, of which the ones from lo[v] to hi - 1 count.  (The last piece of
-// a row ends where the row ends, so that all pieces are whole loads; what it shares
-// with the one before counts there.)
+// start[v] on.  The last piece of a row ends where the row ends, so that all pieces
+// are whole loads; what it shares with the one before has weight 0 in sums,
+// and both lanes store the same values there.
 template <bool kF32, int kVec>
 struct Pieces {
-    static constexpr uint32_t kPer = kF32 ? 4 : 8, kSize = kF32 ? 4 : 2;
+    static constexpr int kPer = kF32 ? 4 : 8;
+    static constexpr uint32_t kSize = kF32 ? 4 : 2;
     uint32_t lanes, sub, held;   // of a row, this lane among them, rows of a wave
-    uint32_t experts, hi;
-    uint32_t start[kVec], lo[kVec];
+    uint32_t experts;
+    uint32_t start[kVec];
+    bool any[kVec];              // whether the lane holds anything there
+    float weight[kVec][kPer];    // 1 or 0
 
     __device__ __forceinline__ explicit Pieces(uint32_t n) : experts(n) {
         const uint32_t pieces = (n + kPer - 1) / kPer;
         lanes = pieces >= 64 ? 64u : pieces > 1 ? 1u << (32 - __clz(pieces - 1)) : 1u;
         sub = threadIdx.x & (lanes - 1);
         held = 64 / lanes;
-        hi = n < kPer ? n : kPer;
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
             const uint32_t first = (sub + 64 * v) * kPer;
             const uint32_t last = n < kPer ? 0 : n - kPer;
             start[v] = first < last ? first : last;
-            lo[v] = first < n ? first - start[v] : kPer;
+            any[v] = first < n;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                weight[v][k] = start[v] + k >= first && start[v] + k < n ? 1.0f : 0.0f;
         }
     }
-    __device__ __forceinline__ bool holds(int v, uint32_t k) const { return k >= lo[v] && k < hi; }
 };
 
-// A row's pieces as they are in memory, at any alignment of their type.
+// What the rows of a wave's turn hold, as it is in memory (at any alignment of its
+// type), and -infinity where a lane holds nothing.
 template <bool kF32, int kVec>
-__device__ __forceinline__ void load_row(word4 (&w)[kVec], const Pieces<kF32, kVec> &P,
-                                         const uint8_t *row) {
-    constexpr uint32_t kPer = Pieces<kF32, kVec>::kPer, kSize = Pieces<kF32, kVec>::kSize;
+struct Turn {
+    static constexpr int kPer = kF32 ? 4 : 8;
+    word4 w[kVec];
+    bool there, live;
+
+    __device__ __forceinline__ void clear() {
+        constexpr uint32_t kFill = kF32 ? 0xFF800000u : 0xFF80FF80u;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-        const uint8_t *p = row + P.start[v] * kSize;
-        if (P.experts >= kPer) {
-            if (P.lo[v] < kPer) w[v] = *(const word4_any *)p;
-            continue;
-        }
+        for (int v = 0; v < kVec; ++v) w[v] = word4{kFill, kFill, kFill, kFill};
+    }
+    __device__ __forceinline__ Turn() : there(false), live(false) { clear(); }
+
+    __device__ __forceinline__ void load(const Pieces<kF32, kVec> &P, const void *logits,
+                                         uint64_t stride, const uint8_t *mask, uint32_t row,
+                                         uint32_t rows) {
+        there = row < rows;
+        live = there && (!mask || mask[row]);
+        if (!there) return;
+        const uint8_t *at = (const uint8_t *)logits + row * stride * P.kSize;
 #pragma unroll
-        for (uint32_t k = 0; k < kPer; ++k) {   // one lane holds the whole row
-            if (k >= P.hi) continue;
-            if constexpr (kF32) w[v][k] = ((const uint32_t *)p)[k];
-            else w[v][k >> 1] = (k & 1 ? w[v][k >> 1] & 0xFFFFu : 0u) |
-                                (uint32_t)((const uint16_t *)p)[k] << (16 * (k & 1));
+        for (int v = 0; v < kVec; ++v) {
+            const uint8_t *p = at + P.start[v] * P.kSize;
+            if (P.experts >= kPer) {
+                if (P.any[v]) w[v] = *(const word4_any *)p;
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {   // one lane holds the whole row
+                if (k >= (int)P.experts) continue;
+                if constexpr (kF32) {
+                    w[v][k] = ((const uint32_t *)p)[k];
+                } else {
+                    const uint32_t e = ((const uint16_t *)p)[k];
+                    w[v][k >> 1] = k & 1 ? (w[v][k >> 1] & 0xFFFFu) | e << 16
+                                         : (w[v][k >> 1] & 0xFFFF0000u) | e;
+                }
+            }
         }
     }
-}
+    // Whatever a row that does not count holds is not looked at.
+    __device__ __forceinline__ void hide() {
+        if (__ballot(!live) && !live) clear();
+    }
+};
 
 // e^(x - m) of the lane's experts, their sum over the row (0: nothing but
 // -infinity, or a row that does not count), and m.
@@ -77,17 +107,12 @@ struct RowSoftmax {
     float e[kVec][kPer];
     float sum, m;
 
-    __device__ __forceinline__ RowSoftmax(const Pieces<kF32, kVec> &P, const word4 (&w)[kVec],
-                                          bool live) {
+    __device__ __forceinline__ RowSoftmax(const Pieces<kF32, kVec> &P, const word4 (&w)[kVec]) {
         m = -INFINITY;
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                e[v][k] = live && k < (int)P.hi && P.lo[v] < P.kPer ? element<kF32>(w[v], k)
-                                                                   : -INFINITY;
-                m = fmaxf(m, e[v][k]);
-            }
+            for (int k = 0; k < kPer; ++k) m = fmaxf(m, element<kF32>(w[v], k));
         m = lanes_reduce<Max>(m, P.lanes);
         if (m == -INFINITY) m = 0.0f;
         float s = 0.0f;
@@ -95,29 +120,13 @@ struct RowSoftmax {
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-                e[v][k] = __builtin_amdgcn_exp2f((e[v][k] - m) * kLog2E);
-                s += P.holds(v, k) ? e[v][k] : 0.0f;
+                e[v][k] = __builtin_amdgcn_exp2f((element<kF32>(w[v], k) - m) * kLog2E);
+                s = fmaf(e[v][k], P.weight[v][k], s);
             }
         sum = lanes_reduce<Add>(s, P.lanes);
     }
-};
-
-// What the rows of a wave's turn hold.  Whatever a row that is not there or does
-// not count holds is not looked at.
-template <bool kF32, int kVec>
-struct Turn {
-    word4 w[kVec];
-    bool there, live;
-
-    __device__ __forceinline__ void load(const Pieces<kF32, kVec> &P, const void *logits,
-                                         uint64_t stride, const uint8_t *mask, uint32_t row,
-                                         uint32_t rows) {
-        there = row < rows;
-        live = false;
-        if (!there) return;
-        live = !mask || mask[row];
-        load_row(w, P, (const uint8_t *)logits + row * stride * P.kSize);
-    }
+    // the hardware's log2, good to one unit in the last place
+    __device__ __forceinline__ float lse() const { return m + kLn2 * __builtin_amdgcn_logf(sum); }
 };
 
 template <bool kF32, int kVec>
@@ -125,16 +134,15 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     constexpr int kPer = kF32 ? 4 : 8;
     constexpr uint32_t kGroupWaves = kBalanceThreads / 64;
     constexpr uint32_t kMost = 64 * kVec * kPer;
-    __shared__ uint32_t s_count[kMost];
-    __shared__ unsigned long long s_p[kMost];
-    __shared__ double s_sum[kGroupWaves];
-    __shared__ uint32_t s_tokens, s_bad_ids, s_bad_rows;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads) {
-        s_count[e] = 0;
-        s_p[e] = 0;
-    }
-    if (threadIdx.x == 0) s_tokens = s_bad_ids = s_bad_rows = 0;
-    __syncthreads();
+    // counts, sums of p, and what else is summed
+    __shared__ unsigned long long s_words[2 * kMost + kSumWords];
+    __shared__ double s_sum[kGroupWaves][3];
+    const uint32_t words = 2 * a.experts + kSumWords;
+    unsigned long long *const s_more = s_words + 2 * a.experts;
+    auto clear = [&] {
+        for (uint32_t i = threadIdx.x; i < words; i += kBalanceThreads) s_words[i] = 0;
+        __syncthreads();
+    };
     const Pieces<kF32, kVec> P(a.experts);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float p[kVec][kPer] = {};
@@ -159,21 +167,23 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     };
     auto count = [&](int64_t id) {
         if (id >= (int64_t)a.experts) bad_id = true;
-        else if (id >= 0) atomicAdd(&s_count[id], 1u);
+        else if (id >= 0) atomicAdd(&s_words[id], 1ull);
     };
-    if (turns) fetch(row);
+    if (turns) fetch(row);   // while the sums are cleared
+    clear();
     for (uint32_t t = 0; t < turns; ++t, row += step) {
-        const Turn<kF32, kVec> now = next;
+        Turn<kF32, kVec> now = next;
         const int64_t id = next_id;
         if (t + 1 < turns) fetch(row + step);
-        const RowSoftmax<kF32, kVec> r(P, now.w, now.live);
+        now.hide();
+        const RowSoftmax<kF32, kVec> r(P, now.w);
         if (r.sum != 0.0f) {   // else nothing, or nothing that counts
-            const float inv = 1.0f / r.sum;
+            const float inv = __builtin_amdgcn_rcpf(r.sum);
 #pragma unroll
             for (int v = 0; v < kVec; ++v)
 #pragma unroll
-                for (int k = 0; k < kPer; ++k) p[v][k] += r.e[v][k] * inv;
-            const float lse = r.m + logf(r.sum);
+                for (int k = 0; k < kPer; ++k) p[v][k] = fmaf(r.e[v][k], inv, p[v][k]);
+            const float lse = r.lse();
             if (P.sub == 0) squares += (double)lse * lse;
             bad_row |= !(r.sum < INFINITY);
         }
@@ -182,78 +192,85 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         count(id);
         for (uint32_t j = P.sub + P.lanes; j < a.choices; j += P.lanes) count(id_at(row, j));
     }
-    if (tokens) atomicAdd(&s_tokens, tokens);
-    if (bad_id) s_bad_ids = 1;
-    if (bad_row) s_bad_rows = 1;
+    if (tokens) atomicAdd(&s_more[kSumTokens], (unsigned long long)tokens);
+    if (bad_id) s_more[kSumBadIds] = 1;
+    if (bad_row) s_more[kSumBadRows] = 1;
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
-            if (P.holds(v, k) && p[v][k] > 0.0f && p[v][k] < INFINITY)
-                atomicAdd(&s_p[P.start[v] + k],
+            if (P.weight[v][k] != 0.0f && p[v][k] > 0.0f && p[v][k] < INFINITY)
+                atomicAdd(&s_words[a.experts + P.start[v] + k],
                           (unsigned long long)__double2ll_rn((double)p[v][k] * kFixed));
-    squares = lanes_reduce<Add>(squares);
-    if (lane == 0) s_sum[wave] = squares;
-    __syncthreads();
-    uint64_t dep = 0;
-    auto add = [&](uint32_t at, uint64_t v) {
-        if (v)
-            dep ^= __hip_atomic_fetch_add(a.sums + at, v, __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT);
-    };
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads) {
-        add(e, s_count[e]);
-        add(a.experts + e, s_p[e]);
-    }
-    if (threadIdx.x == 0) {
-        add(2 * a.experts + kSumTokens, s_tokens);
-        add(2 * a.experts + kSumBadIds, s_bad_ids);
-        add(2 * a.experts + kSumBadRows, s_bad_rows);
-        double all = 0.0;
+    // sums over the workgroup, a value a lane, in a fixed order
+    auto totals = [&](double (&x)[3]) {
 #pragma unroll
-        for (uint32_t w = 0; w < kGroupWaves; ++w) all += s_sum[w];
-        dep ^= __hip_atomic_exchange(a.partial + blockIdx.x, (uint64_t)__double_as_longlong(all),
-                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (!last_of(a.done, gridDim.x, dep)) return;
-
-    // the accumulators are read and cleared
-    auto take = [&](uint32_t at) {
-        return __hip_atomic_exchange(a.sums + at, (uint64_t)0, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
+        for (int k = 0; k < 3; ++k) {
+            x[k] = lanes_reduce<Add>(x[k]);
+            if (lane == 0) s_sum[wave][k] = x[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            x[k] = lanes_reduce<Add>(s_sum[lane & (kGroupWaves - 1)][k], kGroupWaves);
+        __syncthreads();
     };
-    double choices = 0.0, product = 0.0, z = 0.0;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads) {
-        const uint64_t c = take(e);
-        a.counts[e] = (int64_t)c;
-        choices += (double)c;
-        product += (double)c * ((double)take(a.experts + e) / kFixed);
+    double x[3] = {squares, 0.0, 0.0};
+    __syncthreads();
+    if (gridDim.x > 1) {
+        totals(x);
+        // Every workgroup adds to one of kBalanceCopies copies of the sums: additions
+        // to one address by all 256 take 4 us.
+        uint64_t *copy = a.sums + (uint64_t)(blockIdx.x % kBalanceCopies) * words;
+        uint64_t dep = 0;
+        for (uint32_t i = threadIdx.x; i < words; i += kBalanceThreads)
+            if (s_words[i])
+                dep ^= __hip_atomic_fetch_add(copy + i, (uint64_t)s_words[i], __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+        if (threadIdx.x == kBalanceThreads - 1)
+            dep ^= __hip_atomic_exchange(a.partial + blockIdx.x,
+                                         (uint64_t)__double_as_longlong(x[0]), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+        if (!last_of(a.done, gridDim.x, dep)) return;
+        clear();
+        // the copies are read and cleared
+        const uint32_t copies = gridDim.x < kBalanceCopies ? gridDim.x : kBalanceCopies;
+        for (uint32_t i = threadIdx.x; i < copies * words; i += kBalanceThreads) {
+            const uint64_t v = __hip_atomic_exchange(a.sums + i, (uint64_t)0, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT);
+            if (v) atomicAdd(&s_words[i % words], (unsigned long long)v);
+        }
+        static_assert(kBalanceGrid <= kBalanceThreads, "a thread takes one workgroup's sum");
+        x[0] = threadIdx.x < gridDim.x
+                   ? __longlong_as_double((long long)ld_relaxed_agent(a.partial + threadIdx.x))
+                   : 0.0;
+        __syncthreads();
     }
-    static_assert(kBalanceGrid <= kBalanceThreads, "a thread takes one workgroup's sum");
-    if (threadIdx.x < gridDim.x)
-        z = __longlong_as_double((long long)ld_relaxed_agent(a.partial + threadIdx.x));
-    choices = group_total(choices, s_sum);
-    product = group_total(product, s_sum);
-    z = group_total(z, s_sum);
+    // x: the squares, the choices, and sum of c_e sum of p_te
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads) {
+        const uint64_t c = s_words[e];
+        a.counts[e] = (int64_t)c;
+        x[1] += (double)c;
+        x[2] += (double)c * ((double)s_words[a.experts + e] * (1.0 / kFixed));
+    }
+    totals(x);
     if (threadIdx.x == 0) {
-        const uint64_t n = take(2 * a.experts + kSumTokens);
-        const bool bad_ids = take(2 * a.experts + kSumBadIds) != 0;
-        const bool bad_rows = take(2 * a.experts + kSumBadRows) != 0;
+        const uint64_t n = s_more[kSumTokens];
         const double over = n ? 1.0 / (double)n : 0.0;
-        double balance = choices > 0.0 ? (double)a.experts * product / choices * over : 0.0;
-        if (bad_ids || bad_rows) balance = NAN;
-        z *= over;
-        if (bad_rows) z = NAN;
+        double balance = x[1] > 0.0 ? (double)a.experts * x[2] / x[1] * over : 0.0;
+        double z = x[0] * over;
+        if (s_more[kSumBadIds] || s_more[kSumBadRows]) balance = NAN;
+        if (s_more[kSumBadRows]) z = NAN;
         a.result->balance = (float)balance;
         a.result->z = (float)z;
         a.result->loss = (float)(a.balance_coef * balance + a.z_coef * z);
         a.result->tokens = (int64_t)n;
-        __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (gridDim.x > 1)
+            __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
-// A row's pieces from its values.  Two lanes that share experts at a row's end store
-// the same values there.
+// A row's pieces from its values.
 template <bool kF32, int kVec, int kPer>
 __device__ __forceinline__ void store_row(const float (&g)[kVec][kPer],
                                           const Pieces<kF32, kVec> &P, uint8_t *row) {
@@ -266,13 +283,13 @@ __device__ __forceinline__ void store_row(const float (&g)[kVec][kPer],
             if constexpr (kF32) w[k] = __float_as_uint(g[v][k]);
             else w[k] = pack_bf16(g[v][2 * k], g[v][2 * k + 1]);
         }
-        if (P.experts >= P.kPer) {
-            if (P.lo[v] < P.kPer) *(word4_any *)p = w;
+        if (P.experts >= kPer) {
+            if (P.any[v]) *(word4_any *)p = w;
             continue;
         }
 #pragma unroll
-        for (uint32_t k = 0; k < P.kPer; ++k) {
-            if (k >= P.hi) continue;
+        for (int k = 0; k < kPer; ++k) {
+            if (k >= (int)P.experts) continue;
             if constexpr (kF32) ((uint32_t *)p)[k] = w[k];
             else ((uint16_t *)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
         }
@@ -296,57 +313,62 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
     for (uint32_t e = threadIdx.x; e < a.experts; e += kThreads) choices += (double)a.counts[e];
     choices = group_total(choices, s_tmp);
     const double n = *a.tokens > 1 ? (double)*a.tokens : 1.0;
-    const float by_share = (float)(a.scale * a.balance_coef * a.experts / n);
+    // of one choice
+    const double by_share =
+        choices > 0.0 ? a.scale * a.balance_coef * a.experts / n / choices : 0.0;
     const float by_lse = (float)(2.0 * a.scale * a.z_coef / n);
     const float spoilt = a.result && a.result->loss != a.result->loss ? NAN : 0.0f;
-    float share[kVec][kPer];
+    float by[kVec][kPer], held[kVec][kPer];   // an expert's factor, and the same weighted
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            share[v][k] = P.lo[v] < P.kPer && k < (int)P.hi && choices > 0.0
-                              ? (float)((double)a.counts[P.start[v] + k] / choices)
-                              : 0.0f;
+        for (int k = 0; k < kPer; ++k) {
+            const uint32_t e = P.start[v] + k;
+            by[v][k] =
+                P.any[v] && e < a.experts ? (float)(by_share * (double)a.counts[e]) : 0.0f;
+            held[v][k] = by[v][k] * P.weight[v][k];
+        }
     for (uint32_t t = 0; t < turns; ++t, row += step) {
-        const Turn<kF32, kVec> now = next;
+        Turn<kF32, kVec> now = next;
         if (t + 1 < turns) next.load(P, a.logits, a.logits_stride, a.mask, row + step, a.rows);
-        const RowSoftmax<kF32, kVec> r(P, now.w, now.live);
-        const float inv = r.sum != 0.0f ? 1.0f / r.sum : 0.0f;
+        now.hide();
+        const RowSoftmax<kF32, kVec> r(P, now.w);
+        const float inv = r.sum != 0.0f ? __builtin_amdgcn_rcpf(r.sum) : 0.0f;
         float inner = 0.0f;
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                inner += P.holds(v, k) ? r.e[v][k] * share[v][k] : 0.0f;
+            for (int k = 0; k < kPer; ++k) inner = fmaf(r.e[v][k], held[v][k], inner);
         inner = lanes_reduce<Add>(inner, P.lanes) * inv;
-        const float same = (r.sum != 0.0f ? by_lse * (r.m + logf(r.sum)) : 0.0f) - by_share * inner;
+        float same = r.sum != 0.0f ? by_lse * r.lse() - inner : 0.0f;
+        if (now.live) same += spoilt;
         if (!now.there) continue;
         float g[kVec][kPer];
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                g[v][k] = now.live ? r.e[v][k] * inv * (by_share * share[v][k] + same) + spoilt
-                                   : 0.0f;
+            for (int k = 0; k < kPer; ++k) g[v][k] = r.e[v][k] * inv * (by[v][k] + same);
         store_row(g, P, (uint8_t *)a.out + row * a.out_stride * P.kSize);
     }
 }
 
-// workgroups of `waves` waves for the rows: `most`, or a turn each
-uint32_t grid_of(uint32_t rows, uint32_t experts, bool f32, uint32_t waves, uint32_t most) {
+// workgroups of `waves` waves for the rows: `most`, or a turn each, or one for up to
+// `alone` turns
+uint32_t grid_of(uint32_t rows, uint32_t experts, bool f32, uint32_t waves, uint32_t most,
+                 uint32_t alone) {
     const uint32_t per = f32 ? 4 : 8, pieces = (experts + per - 1) / per;
     uint32_t lanes = 1;
     while (lanes < 64 && lanes < pieces) lanes *= 2;
     const uint32_t turn = waves * (64 / lanes);
-    const uint32_t groups = (rows + turn - 1) / turn;
-    return groups < most ? (groups ? groups : 1) : most;
+    const uint32_t turns = (rows + turn - 1) / turn;
+    return turns <= alone ? 1 : turns < most ? turns : most;
 }
 
 }  // namespace
 
 hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream) {
     const uint32_t grid =
-        grid_of(a.rows, a.experts, f32, kBalanceThreads / 64, kBalanceGrid);
+        grid_of(a.rows, a.experts, f32, kBalanceThreads / 64, kBalanceGrid, kBalanceAlone);
     auto *kernel = f32 ? (a.experts <= 256   ? balance_kernel<true, 1>
                           : a.experts <= 512 ? balance_kernel<true, 2>
                                              : balance_kernel<true, 4>)
@@ -355,7 +377,7 @@ hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream) {
 }
 
 hipError_t launch_balance_backward(const BalanceGradArgs &a, bool f32, hipStream_t stream) {
-    const uint32_t grid = grid_of(a.rows, a.experts, f32, kWaves, kBalanceGradGrid);
+    const uint32_t grid = grid_of(a.rows, a.experts, f32, kWaves, kBalanceGradGrid, 1);
     auto *kernel =
         f32 ? (a.experts <= 256   ? balance_grad_kernel<true, 1>
                : a.experts <= 512 ? balance_grad_kernel<true, 2>

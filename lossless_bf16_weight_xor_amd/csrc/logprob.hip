@@ -43,101 +43,29 @@ __device__ __forceinline__ void merge(Sums &a, Sums b, float c) {
     a.w += b.w;
 }
 // the sums of the whole workgroup, in every thread
-__device__ __forceinline__ Sums group_sums(Sums a, float c, float (*s_tmp)[3]) {
-    shift(a, lanes_reduce<Max>(a.m), c);
-    a.s = lanes_reduce<Add>(a.s);
-    a.w = lanes_reduce<Add>(a.w);
-    const uint32_t wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
+template <uint32_t kCount>
+__device__ __forceinline__ Sums group_sums(Sums a, float c, float (&s_tmp)[kCount][3]) {
+    auto reduce = [&](Sums &x, uint32_t lanes) {
+        shift(x, lanes_reduce<Max>(x.m, lanes), c);
+        x.s = lanes_reduce<Add>(x.s, lanes);
+        x.w = lanes_reduce<Add>(x.w, lanes);
+    };
+    reduce(a, 64);
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane == 0) {
         s_tmp[wave][0] = a.m;
         s_tmp[wave][1] = a.s;
         s_tmp[wave][2] = a.w;
     }
     __syncthreads();
-    Sums all = {s_tmp[0][0], s_tmp[0][1], s_tmp[0][2]};
-#pragma unroll
-    for (uint32_t v = 1; v < kWaves; ++v)
-        merge(all, Sums{s_tmp[v][0], s_tmp[v][1], s_tmp[v][2]}, c);
+    const float *of = s_tmp[lane & (kCount - 1)];
+    Sums all = {of[0], of[1], of[2]};
+    reduce(all, kCount);
     __syncthreads();
     return all;
 }
 
-// ---- the largest elements -------------------------------------------------------------
-// A wave keeps the largest it has seen as one key a lane, sorted from lane 0
-// down: the value's order in the high word, the complement of its id in the
-// low one, so that no two are equal and the lower id of equal values is the
-// larger key.  0 is no element.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t id) {
-    if (!(x > -INFINITY)) return 0;
-    const uint32_t b = __float_as_uint(x + 0.0f);   // -0 counts as 0
-    const uint32_t order = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return (uint64_t)order << 32 | (uint32_t)~id;
-}
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t o = (uint32_t)(key >> 32);
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-__device__ __forceinline__ uint64_t shfl_key(uint64_t k, uint32_t lane) {
-    return __shfl((unsigned long long)k, (int)lane, 64);
-}
-__device__ __forceinline__ uint64_t readlane_key(uint64_t k, uint32_t lane) {
-    return (uint64_t)readlane_u32((uint32_t)k, lane) |
-           (uint64_t)readlane_u32((uint32_t)(k >> 32), lane) << 32;
-}
-// the 64 largest of two sorted lists, sorted
-__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b) {
-    const uint32_t lane = threadIdx.x & 63;
-    const uint64_t r = shfl_key(b, 63 - lane);
-    uint64_t c = a > r ? a : r;   // falls and rises, or rises and falls
-#pragma unroll
-    for (uint32_t d = 32; d >= 1; d >>= 1) {
-        const uint64_t o = shfl_key(c, lane ^ d);
-        const bool keep_larger = (lane & d) == 0;
-        c = (c > o) == keep_larger ? c : o;
-    }
-    return c;
-}
-// the value of rank `rank` (from 0) among the lanes' values, NaN aside
-__device__ __forceinline__ float ranked_value(float v, uint32_t rank) {
-    const uint32_t lane = threadIdx.x & 63;
-    v = v > -INFINITY ? v : -INFINITY;
-#pragma unroll
-    for (uint32_t size = 2; size <= 64; size <<= 1) {
-#pragma unroll
-        for (uint32_t d = size >> 1; d >= 1; d >>= 1) {
-            const float o = __shfl_xor(v, (int)d, 64);
-            const bool falling = (lane & size) == 0;   // (lane & 64) is 0 at the last size
-            const bool keep_larger = ((lane & d) == 0) == falling;
-            v = keep_larger ? fmaxf(v, o) : fminf(v, o);
-        }
-    }
-    return __uint_as_float(readlane_u32(__float_as_uint(v), rank));
-}
-
-struct TopList {
-    uint64_t key;        // this lane's
-    uint64_t last;       // the key of the last place that counts, 0 while it is free
-    float least;         // what an element has to reach
-};
-// one candidate a lane (0: none), of any number
-__device__ __forceinline__ void insert(TopList &l, uint64_t key, uint32_t top) {
-    const uint32_t lane = threadIdx.x & 63;
-    uint64_t todo = __ballot(key > l.last);
-    while (todo) {
-        const uint32_t from = (uint32_t)__builtin_ctzll(todo);
-        const uint64_t k = readlane_key(key, from);
-        const uint32_t place = (uint32_t)__popcll(__ballot(l.key > k));
-        const uint64_t before = (uint64_t)wave_shr1((uint32_t)l.key) |
-                                (uint64_t)wave_shr1((uint32_t)(l.key >> 32)) << 32;
-        l.key = lane < place ? l.key : lane == place ? k : before;
-        l.last = readlane_key(l.key, top - 1);
-        todo &= todo - 1;
-        todo &= __ballot(key > l.last);
-    }
-    if (l.last) l.least = fmaxf(l.least, key_value(l.last));
-}
-
-// ---- forward ---------------------------------------------------------------------------
+// ---- rows of logits ---------------------------------------------------------------------
 // A row is cut into vectors at 16-byte addresses: vector i holds its elements from
 // i * kPer - skip on, skip being how many elements lie between such an address
 // and the row's start.  Only the first and the last vector can be partial.
@@ -158,14 +86,26 @@ struct RowVectors {
     __device__ __forceinline__ bool whole(uint32_t i) const {
         return first(i) < vocab && vocab - first(i) >= kPer;
     }
-    // whether every vector of the turn is
+    // whether every vector of a turn of kBlock threads is
+    template <uint32_t kBlock>
     __device__ __forceinline__ bool whole_turn(uint32_t turn) const {
-        return (turn > 0 || skip == 0) && (turn + 1) * kTurnVectors * kPer <= vocab + skip;
+        return (turn > 0 || skip == 0) && (turn + 1) * kTurnVectors * kBlock * kPer <= vocab + skip;
     }
+    __device__ __forceinline__ uint32_t vectors() const { return (vocab + skip + kPer - 1) / kPer; }
+    template <uint32_t kBlock>
     __device__ __forceinline__ uint32_t turns() const {
-        return (vocab + skip + kTurnVectors * kPer - 1) / (kTurnVectors * kPer);
+        constexpr uint32_t kTurn = kTurnVectors * kBlock;
+        return (vectors() + kTurn - 1) / kTurn;
     }
 };
+
+// The same vector, as one the compiler has not seen: it widens bf16 elements again
+// where they are used, and does not keep them widened, so that 64 registers
+// are enough for two workgroups of 16 waves on a CU.
+__device__ __forceinline__ word4 fresh(word4 w) {
+    asm volatile("" : "+v"(w));
+    return w;
+}
 
 // what is no token is -infinity
 template <bool kF32>
@@ -188,28 +128,235 @@ __device__ __forceinline__ word4 load_partial(const RowVectors<kF32> &r, uint32_
     return w;
 }
 
-// The thread's vectors of a turn (vector q * kThreads + threadIdx.x of it).  kKeep: they
+// The thread's vectors of a turn (vector q * kBlock + threadIdx.x of it).  kKeep: they
 // may stay in the caches.
-template <bool kKeep, bool kF32>
+template <uint32_t kBlock, bool kKeep, bool kF32>
 __device__ __forceinline__ void load_turn(word4 (&v)[4], const RowVectors<kF32> &r,
                                           uint32_t turn) {
-    const uint32_t first = turn * kTurnVectors + threadIdx.x;
-    if (r.whole_turn(turn)) {
+    const uint32_t first = turn * kTurnVectors * kBlock + threadIdx.x;
+    if (r.template whole_turn<kBlock>(turn)) {
         const auto *p = (const word4 *)r.at(first);
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q) {
-            if constexpr (kKeep) v[q] = p[q * kThreads];
-            else v[q] = __builtin_nontemporal_load(p + q * kThreads);
+            if constexpr (kKeep) v[q] = p[q * kBlock];
+            else v[q] = __builtin_nontemporal_load(p + q * kBlock);
         }
         return;
     }
+    constexpr uint32_t kFill = kF32 ? 0xFF800000u : 0xFF80FF80u;
+    bool partial = false;
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-        const uint32_t i = first + q * kThreads;
-        v[q] = r.whole(i) ? *(const word4 *)r.at(i) : load_partial(r, i);
+        const uint32_t i = first + q * kBlock;
+        v[q] = word4{kFill, kFill, kFill, kFill};
+        if (r.whole(i)) v[q] = *(const word4 *)r.at(i);
+        else partial |= i < r.vectors();
+    }
+    if (!partial) return;
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+        const uint32_t i = first + q * kBlock;
+        if (i < r.vectors() && !r.whole(i)) v[q] = fresh(load_partial(r, i));   // one at a time
     }
 }
 
+// ---- the largest elements -------------------------------------------------------------
+// An element as one key: the value's order in the high word, the complement of
+// its id in the low one, so that no two are equal and the lower id of equal
+// values is the larger key.  0 is no element.  Lists are a wave's lanes, the largest
+// key in lane 0.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t id) {
+    if (!(x > -INFINITY)) return 0;
+    const uint32_t b = __float_as_uint(x + 0.0f);   // -0 counts as 0
+    const uint32_t order = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    return (uint64_t)order << 32 | (uint32_t)~id;
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t o = (uint32_t)(key >> 32);
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ uint64_t readlane_key(uint64_t k, uint32_t lane) {
+    return (uint64_t)readlane_u32((uint32_t)k, lane) |
+           (uint64_t)readlane_u32((uint32_t)(k >> 32), lane) << 32;
+}
+
+// One comparison of a sorting network: the lower lane of a pair keeps the larger.
+template <int kMask>
+__device__ __forceinline__ bool lower_lane() {
+    return (threadIdx.x & (1u << (31 - __builtin_clz(kMask)))) == 0;
+}
+template <int kMask>
+__device__ __forceinline__ void exchange(float &v) {
+    const float o = __uint_as_float(lane_xor<kMask>(__float_as_uint(v)));
+    v = lower_lane<kMask>() ? fmaxf(v, o) : fminf(v, o);
+}
+template <int kMask>
+__device__ __forceinline__ uint64_t xor_key(uint64_t v) {
+    return (uint64_t)lane_xor<kMask>((uint32_t)(v >> 32)) << 32 | lane_xor<kMask>((uint32_t)v);
+}
+template <int kMask>
+__device__ __forceinline__ void exchange(uint64_t &v) {
+    const uint64_t o = xor_key<kMask>(v);
+    v = (v > o) == lower_lane<kMask>() ? v : o;
+}
+// sorts what first rises and then falls, or the other way round, over kSize lanes
+template <int kSize, typename T>
+__device__ __forceinline__ void merge_halves(T &v) {
+    if constexpr (kSize > 1) {
+        exchange<kSize / 2>(v);
+        merge_halves<kSize / 2>(v);
+    }
+}
+// sorts the values of kSize lanes (not NaN)
+template <int kSize = 64, typename T>
+__device__ __forceinline__ void sort_lanes(T &v) {
+    if constexpr (kSize > 1) {
+        sort_lanes<kSize / 2>(v);
+        exchange<kSize - 1>(v);
+        merge_halves<kSize / 2>(v);
+    }
+}
+// the 64 largest of two lists
+__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b) {
+    const uint64_t r = xor_key<63>(b);
+    uint64_t c = a > r ? a : r;
+    merge_halves<64>(c);
+    return c;
+}
+
+// Inserts one candidate a lane (0: none), of any number; `last`: the key of the
+// list's last place that counts, 0 while it is free.
+__device__ __forceinline__ void insert(uint64_t &list, uint64_t &last, uint64_t key, uint32_t top) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint64_t todo = __ballot(key > last);
+    while (todo) {
+        const uint32_t from = (uint32_t)__builtin_ctzll(todo);
+        const uint64_t k = readlane_key(key, from);
+        const uint32_t place = (uint32_t)__popcll(__ballot(list > k));
+        const uint64_t before = (uint64_t)wave_shr1((uint32_t)list) |
+                                (uint64_t)wave_shr1((uint32_t)(list >> 32)) << 32;
+        list = lane < place ? list : lane == place ? k : before;
+        last = readlane_key(list, top - 1);
+        todo &= todo - 1;
+        todo &= __ballot(key > last);
+    }
+}
+
+// A workgroup's largest elements.  In each turn the lanes' maxima are joined to 16, 32
+// or 64 groups; the group maximum of rank `top` is a bound that `top` elements
+// reach.  Those that reach it (hardly more, unless many are equal or `top` is near
+// 64) are collected and put in order.
+constexpr uint32_t kFound = 1024;
+template <uint32_t kCount>   // waves
+struct TopShared {
+    float named[64];
+    float bound;
+    uint32_t count[2];   // of the found ones, for even and odd turns
+    float least;         // what an element has to reach to be among the largest so far
+    uint64_t found[kFound];
+    uint64_t lists[kCount][64];
+};
+// One wave: the list of the keys of its first `count` lanes, which s.found holds, too
+// (the others' are 0).  A key's place is how many are larger; a sorting network
+// takes twice as long for the 10 to 30 keys that there are as a rule.
+template <uint32_t kCount>
+__device__ __forceinline__ uint64_t in_order(TopShared<kCount> &s, uint64_t key, uint32_t count) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t place = 0;
+#pragma unroll 4
+    for (uint32_t j = 0; j < count; ++j) place += s.found[j] > key;
+    if (lane < count) s.lists[0][place] = key;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // a wave's LDS accesses are in order
+    return lane < count ? s.lists[0][lane] : 0;
+}
+// v: the thread's vectors of the turn, m: their maxima; begin: the first turn
+template <uint32_t kCount, bool kF32>
+__device__ __forceinline__ void add_largest(uint64_t &list, TopShared<kCount> &s,
+                                            const word4 (&v)[4], const float (&m)[4],
+                                            const RowVectors<kF32> &r, uint32_t turn,
+                                            bool begin, uint32_t top) {
+    constexpr int kPer = kF32 ? 4 : 8;
+    constexpr uint32_t kBlock = 64 * kCount;
+    static_assert(kBlock == 1024 && kFound <= kBlock, "groups of 16 to 64 lanes");
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, even = turn & 1;
+    const uint32_t first = turn * kTurnVectors * kBlock + threadIdx.x;
+    // With 64 groups of a row in no order and top 20, 24 elements reach the bound;
+    // with 16 and 8, 11.  A turn with fewer vectors than threads has groups of fewer
+    // lanes, enough of them for `top`.
+    const uint32_t groups = top <= 8 ? 16 : top <= 16 ? 32 : 64;
+    const uint32_t vectors = r.vectors() - turn * kTurnVectors * kBlock;
+    uint32_t group = kBlock / groups;
+    while (group > 1 && vectors < group * umax32(top, groups / 2)) group >>= 1;
+    float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    most = most > -INFINITY ? most : -INFINITY;   // no NaN
+    const float joined = lanes_reduce<Max>(most, group);
+    if (threadIdx.x < groups * group && (threadIdx.x & (group - 1)) == 0)
+        s.named[threadIdx.x / group] = joined;
+    if (threadIdx.x == 0) s.count[even] = 0;
+    __syncthreads();
+    if (wave == 0) {   // a sort by all waves takes 0.7 us longer
+        float x = lane < groups ? s.named[lane] : -INFINITY;
+        if (groups == 16) sort_lanes<16>(x);
+        else if (groups == 32) sort_lanes<32>(x);
+        else sort_lanes<64>(x);
+        const float bound = __uint_as_float(readlane_u32(__float_as_uint(x), top - 1));
+        if (lane == 0) s.bound = begin ? bound : fmaxf(bound, s.least);
+    }
+    __syncthreads();
+    const float bound = s.bound;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (!__ballot(m[q] >= bound)) continue;
+        const word4 w = fresh(v[q]);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const float e = element<kF32>(w, k);
+            if (!(e >= bound && e > -INFINITY)) continue;
+            const uint32_t place = atomicAdd(&s.count[even], 1u);
+            if (place < kFound) s.found[place] = key_of(e, r.first(first + q * kBlock) + k);
+        }
+    }
+    __syncthreads();
+    const uint32_t count = s.count[even];
+    if (count <= 64) {
+        if (wave == 0) {
+            const uint64_t sorted = in_order(s, lane < count ? s.found[lane] : 0, count);
+            list = begin ? sorted : merge_lists(list, sorted);
+        }
+    } else {
+        uint64_t mine = 0;
+        if (count <= kFound) {
+            if (64 * wave < count) {
+                mine = threadIdx.x < count ? s.found[threadIdx.x] : 0;
+                sort_lanes(mine);
+            }
+        } else {   // more than that are equal, or nearly: each wave keeps a list
+            uint64_t last = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const word4 w = fresh(v[q]);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const float e = element<kF32>(w, k);
+                    if (!__ballot(e >= bound)) continue;
+                    insert(mine, last,
+                           e >= bound ? key_of(e, r.first(first + q * kBlock) + k) : 0, top);
+                }
+            }
+        }
+        s.lists[wave][lane] = mine;
+        __syncthreads();
+        if (wave == 0)
+            for (uint32_t w = 0; w < kCount && (64 * w < count || count > kFound); ++w)
+                list = merge_lists(list, s.lists[w][lane]);
+    }
+    if (wave == 0) {
+        const uint64_t last = readlane_key(list, top - 1);
+        if (lane == 0) s.least = last ? key_value(last) : -INFINITY;
+    }
+}
+
+// ---- forward ---------------------------------------------------------------------------
 template <bool kF32, bool kEntropy>
 __device__ __forceinline__ void add_turn(Sums &a, const word4 (&v)[4], float m, float c) {
     constexpr int kPer = kF32 ? 4 : 8;
@@ -260,109 +407,110 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, uint32_t row, co
     }
 }
 
-template <bool kF32, bool kEntropy, bool kTop, bool kKeep>
-__global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
-    __shared__ float s_tmp[kWaves][3];
-    __shared__ uint64_t s_list[kTop ? kWaves : 1][64];
+template <uint32_t kBlock, bool kF32, bool kEntropy, bool kTop, bool kKeep>
+__global__ __launch_bounds__(kBlock, kTop ? 8 : 1) void logprob_kernel(LogprobArgs a) {
+    constexpr uint32_t kCount = kBlock / 64;
+    __shared__ float s_tmp[kCount][3];
+    __shared__ TopShared<kTop ? kCount : 1> s_top;
     constexpr uint32_t kPer = kF32 ? 4 : 8, kSize = kF32 ? 4 : 2;
-    const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
+    const uint32_t row = scalar_div(blockIdx.x, a.parts), part = blockIdx.x - row * a.parts;
+    const RowVectors<kF32> r(row_ptr(a.logits, row, a.inner, kSize), a.vocab);
+    const uint32_t turns = r.template turns<kBlock>();
+    const uint32_t begin = part * a.part_turns;
+    const uint32_t end = begin + a.part_turns < turns ? begin + a.part_turns : turns;
+    // Few rows, hardly more than a turn each: the first one is not kept waiting for the
+    // token.  Many: a row that is left out is not read, and a turn's vectors are
+    // loaded a turn ahead.
+    constexpr bool kWide = kBlock > kThreads;
+    word4 v[4], next[4];
+    auto load = [&](uint32_t turn) { load_turn<kBlock, kKeep>(kWide ? v : next, r, turn); };
+    if (kWide && begin < end) load(begin);
     const int64_t token =
         load_id(row_ptr(a.tokens, row, a.inner, a.token_i32 ? 4 : 8), a.token_i32);
     if (token < 0) {
         if (part == 0) write_left_out(a, row);
         return;
     }
-    const uint8_t *x = row_ptr(a.logits, row, a.inner, kSize);
+    if (!kWide && begin < end) load(begin);
     float own = 0.0f;   // the token's logit
     if (threadIdx.x == 0 && token < (int64_t)a.vocab) {
-        if constexpr (kF32) own = ((const float *)x)[token];
-        else own = __uint_as_float((uint32_t)((const uint16_t *)x)[token] << 16);
+        if constexpr (kF32) own = ((const float *)r.row)[token];
+        else own = __uint_as_float((uint32_t)((const uint16_t *)r.row)[token] << 16);
     }
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const RowVectors<kF32> r(x, a.vocab);
-    const uint32_t turns = r.turns();
-    const uint32_t begin = part * a.part_turns;
-    const uint32_t end = begin + a.part_turns < turns ? begin + a.part_turns : turns;
     Sums mine = {-INFINITY, 0.0f, 0.0f};
-    TopList best = {0, 0, -INFINITY};
-    word4 v[4], next[4];
-    if (begin < end) load_turn<kKeep>(next, r, begin);
+    uint64_t list = 0;   // the first wave's
     for (uint32_t turn = begin; turn < end; ++turn) {
+        if constexpr (!kWide) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = next[q];
-        if (turn + 1 < end) load_turn<kKeep>(next, r, turn + 1);
-        float m = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int k = 0; k < (int)kPer; ++k) m = fmaxf(m, element<kF32>(v[q], k));
-        if constexpr (kTop) {
-            if (__ballot(m >= best.least && m > -INFINITY)) {
-                // at least `top` elements reach the maximum of that rank
-                if (!best.last) best.least = fmaxf(best.least, ranked_value(m, a.top - 1));
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int k = 0; k < (int)kPer; ++k) {
-                        const float e = element<kF32>(v[q], k);
-                        if (!__ballot(e >= best.least)) continue;
-                        const uint32_t id =
-                            r.first(turn * kTurnVectors + q * kThreads + threadIdx.x) + k;
-                        insert(best, e >= best.least ? key_of(e, id) : 0, a.top);
-                    }
-            }
+            for (int q = 0; q < 4; ++q) v[q] = next[q];
+            if (turn + 1 < end) load(turn + 1);
         }
-        add_turn<kF32, kEntropy>(mine, v, m, a.scale);
+        float m[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            m[q] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < (int)kPer; ++k) m[q] = fmaxf(m[q], element<kF32>(v[q], k));
+        }
+        if constexpr (kTop) add_largest(list, s_top, v, m, r, turn, turn == begin, a.top);
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        if constexpr (kTop) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = fresh(v[q]);
+        }
+        add_turn<kF32, kEntropy>(mine, v, most, a.scale);
+        if constexpr (kWide) {
+            if (turn + 1 < end) load(turn + 1);
+        }
     }
     Sums all = group_sums(mine, a.scale, s_tmp);
-    uint64_t key = 0;
-    if constexpr (kTop) {
-        s_list[wave][lane] = best.key;
-        __syncthreads();
-        key = s_list[0][lane];
-#pragma unroll
-        for (uint32_t v = 1; v < kWaves; ++v) key = merge_lists(key, s_list[v][lane]);
-    }
     if (a.parts == 1) {
-        write_row<kEntropy>(a, row, all, token, own, key);
+        write_row<kEntropy>(a, row, all, token, own, list);
         return;
     }
     // the part's sums and list are handed over by returning device-scope atomics
     const uint32_t words = 2 + a.top;
     uint64_t *mine_at = a.partial + (uint64_t)blockIdx.x * words;
     uint64_t dep = 0;
-    auto hand = [&](uint32_t at, uint64_t v) {
-        return __hip_atomic_exchange(mine_at + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    };
-    if (wave == 0) {
-        if (lane == 0)
-            dep = hand(0, (uint64_t)__float_as_uint(all.m) << 32 | __float_as_uint(all.s));
-        if (lane == 1) dep = hand(1, __float_as_uint(all.w));
-        if (kTop && lane < a.top) dep += hand(2 + lane, key);
+    if (threadIdx.x < words) {   // the first wave, and two lanes more
+        uint64_t w = list;
+        if (threadIdx.x >= a.top)
+            w = threadIdx.x == a.top ? (uint64_t)__float_as_uint(all.m) << 32 | __float_as_uint(all.s)
+                                     : __float_as_uint(all.w);
+        dep = __hip_atomic_exchange(mine_at + threadIdx.x, w, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
     }
     if (!last_of(a.done + row, a.parts, dep)) return;
     const uint64_t *row_at = a.partial + (uint64_t)row * a.parts * words;
     mine = Sums{-INFINITY, 0.0f, 0.0f};
-    for (uint32_t p = threadIdx.x; p < a.parts; p += kThreads) {
-        const uint64_t ms = ld_relaxed_agent(row_at + (uint64_t)p * words);
-        const uint64_t w = ld_relaxed_agent(row_at + (uint64_t)p * words + 1);
+    for (uint32_t p = threadIdx.x; p < a.parts; p += kBlock) {
+        const uint64_t *at = row_at + (uint64_t)p * words + a.top;
+        const uint64_t ms = ld_relaxed_agent(at), w = ld_relaxed_agent(at + 1);
         merge(mine, Sums{__uint_as_float((uint32_t)(ms >> 32)), __uint_as_float((uint32_t)ms),
                          __uint_as_float((uint32_t)w)}, a.scale);
     }
-    all = group_sums(mine, a.scale, s_tmp);
     if constexpr (kTop) {
-        key = 0;
-        for (uint32_t p = wave; p < a.parts; p += kWaves)
-            key = merge_lists(key, lane < a.top ? ld_relaxed_agent(row_at + (uint64_t)p * words +
-                                                                   2 + lane)
-                                                : 0);
-        s_list[wave][lane] = key;
+        // the parts' keys, 64 a wave in turn
+        const uint32_t keys = a.parts * a.top;
+        list = 0;
+        for (uint32_t k = 64 * wave; k < keys; k += kBlock) {
+            uint64_t key = 0;
+            if (k + lane < keys) {
+                const uint32_t p = (k + lane) / a.top;
+                key = ld_relaxed_agent(row_at + (uint64_t)p * words + (k + lane - p * a.top));
+            }
+            sort_lanes(key);
+            list = merge_lists(list, key);
+        }
+        s_top.lists[wave][lane] = list;
         __syncthreads();
-        key = s_list[0][lane];
-#pragma unroll
-        for (uint32_t v = 1; v < kWaves; ++v) key = merge_lists(key, s_list[v][lane]);
+        if (wave == 0)
+            for (uint32_t w = 1; w < kCount && 64 * w < keys; ++w)
+                list = merge_lists(list, s_top.lists[w][lane]);
     }
-    write_row<kEntropy>(a, row, all, token, own, key);
+    all = group_sums(mine, a.scale, s_tmp);
+    write_row<kEntropy>(a, row, all, token, own, list);
     if (threadIdx.x == 0)
         __hip_atomic_store(a.done + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -375,7 +523,7 @@ __device__ __forceinline__ void store_turn(const word4 (&v)[4], uint8_t *out,
     constexpr uint32_t kPer = RowVectors<kF32>::kPer, kSize = RowVectors<kF32>::kSize;
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-        const uint32_t i = turn * kTurnVectors + threadIdx.x + q * kThreads;
+        const uint32_t i = turn * kTurnVectors * kThreads + threadIdx.x + q * kThreads;
         const uint32_t first = r.first(i);
         if (r.whole(i)) {
             __builtin_nontemporal_store(v[q], (word4_any *)(out + (uint64_t)first * kSize));
@@ -395,12 +543,12 @@ __device__ __forceinline__ void store_turn(const word4 (&v)[4], uint8_t *out,
 template <bool kF32, bool kEntropy>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs g) {
     constexpr uint32_t kPer = kF32 ? 4 : 8, kSize = kF32 ? 4 : 2;
-    const uint32_t row = blockIdx.x / g.parts, part = blockIdx.x - row * g.parts;
+    const uint32_t row = scalar_div(blockIdx.x, g.parts), part = blockIdx.x - row * g.parts;
     const int64_t token =
         load_id(row_ptr(g.tokens, row, g.inner, g.token_i32 ? 4 : 8), g.token_i32);
     uint8_t *out = const_cast<uint8_t *>(row_ptr(g.out, row, g.inner, kSize));
     const RowVectors<kF32> r(row_ptr(g.logits, row, g.inner, kSize), g.vocab);
-    const uint32_t turns = r.turns();
+    const uint32_t turns = r.template turns<kThreads>();
     const uint32_t begin = part * g.part_turns;
     const uint32_t end = begin + g.part_turns < turns ? begin + g.part_turns : turns;
     const float a = g.grad_logp[row], h = kEntropy ? g.grad_entropy[row] : 0.0f;
@@ -420,10 +568,10 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
     const float B = -h * inv_t * kLn2;
     for (uint32_t turn = begin; turn < end; ++turn) {
         word4 v[4];
-        load_turn<false>(v, r, turn);
+        load_turn<kThreads, false>(v, r, turn);
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q) {
-            const uint32_t id = r.first(turn * kTurnVectors + q * kThreads + threadIdx.x);
+            const uint32_t id = r.first((turn * kTurnVectors + q) * kThreads + threadIdx.x);
             const uint32_t hit = (uint32_t)token - id;   // below kPer: the token is here
             float d[kPer];
 #pragma unroll
@@ -446,21 +594,23 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
 }
 
 template <bool kF32, bool kEntropy>
-hipError_t launch_forward(const LogprobArgs &a, bool keep, hipStream_t stream) {
-    // few rows have alternatives: they stay in the caches in any case
-    auto *kernel = a.top  ? logprob_kernel<kF32, kEntropy, true, true>
-                   : keep ? logprob_kernel<kF32, kEntropy, false, true>
-                          : logprob_kernel<kF32, kEntropy, false, false>;
-    return launch_one(kernel, a.rows * a.parts, kThreads, a, 0, stream);
+hipError_t launch_forward(const LogprobArgs &a, bool wide, bool keep, hipStream_t stream) {
+    auto *kernel = a.top  ? logprob_kernel<kLogprobWide, kF32, kEntropy, true, true>
+                   : wide ? logprob_kernel<kLogprobWide, kF32, kEntropy, false, true>
+                   : keep ? logprob_kernel<kThreads, kF32, kEntropy, false, true>
+                          : logprob_kernel<kThreads, kF32, kEntropy, false, false>;
+    return launch_one(kernel, a.rows * a.parts, wide ? kLogprobWide : kThreads, a, 0, stream);
 }
+
 }  // namespace
 
-hipError_t launch_logprob(const LogprobArgs &a, bool f32, bool keep, hipStream_t stream) {
+hipError_t launch_logprob(const LogprobArgs &a, bool f32, bool wide, bool keep,
+                          hipStream_t stream) {
     if (f32)
-        return a.entropy ? launch_forward<true, true>(a, keep, stream)
-                         : launch_forward<true, false>(a, keep, stream);
-    return a.entropy ? launch_forward<false, true>(a, keep, stream)
-                     : launch_forward<false, false>(a, keep, stream);
+        return a.entropy ? launch_forward<true, true>(a, wide, keep, stream)
+                         : launch_forward<true, false>(a, wide, keep, stream);
+    return a.entropy ? launch_forward<false, true>(a, wide, keep, stream)
+                     : launch_forward<false, false>(a, wide, keep, stream);
 }
 
 hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream_t stream) {

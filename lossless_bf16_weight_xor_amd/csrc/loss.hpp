@@ -14,12 +14,15 @@ namespace bf16d {
 // A row is read in turns: four 16-byte vectors a thread.  Rows are cut into
 // parts of whole turns, one workgroup each, where there are fewer rows than
 // kLogprobGroups.
-constexpr uint32_t kTurnVectors = 4 * kThreads;
-constexpr uint32_t kLogprobGroups = 1024;
+constexpr uint32_t kTurnVectors = 4;   // of a thread
+constexpr uint32_t kLogprobGroups = 256;
+constexpr uint32_t kLogprobWide = 1024;        // threads
+constexpr uint32_t kLogprobWideGroups = 512;
 constexpr uint32_t vector_elems(uint32_t dtype) { return dtype == BF16D_LOGITS_F32 ? 4 : 8; }
-// The most turns of a row; aligned: all rows start at 16-byte addresses.
-inline uint32_t turns_of(uint32_t vocab, uint32_t dtype, bool aligned) {
-    const uint32_t per = kTurnVectors * vector_elems(dtype);
+// The most turns of a row for workgroups of `threads`; aligned: all rows start at
+// 16-byte addresses.
+inline uint32_t turns_of(uint32_t vocab, uint32_t dtype, bool aligned, uint32_t threads) {
+    const uint32_t per = kTurnVectors * threads * vector_elems(dtype);
     return (vocab + (aligned ? 0 : vector_elems(dtype) - 1) + per - 1) / per;
 }
 // Logits of up to this many bytes are left in the last-level cache for the
@@ -45,8 +48,10 @@ struct LogprobArgs {
     uint64_t *partial;   // (2 + top) words of each part of each row
     uint32_t *done;      // of each row
 };
-// keep: the logits may stay in the caches
-hipError_t launch_logprob(const LogprobArgs &a, bool f32, bool keep, hipStream_t stream);
+// wide: workgroups of kLogprobWide threads (with alternatives: always); keep: the
+// logits may stay in the caches (with wide: always)
+hipError_t launch_logprob(const LogprobArgs &a, bool f32, bool wide, bool keep,
+                          hipStream_t stream);
 
 struct LogprobGradArgs {
     RowSet logits, tokens, out;
@@ -60,6 +65,7 @@ hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream
 // ---- policy loss ----------------------------------------------------------------
 constexpr uint32_t kPolicyGrid = 256;
 constexpr uint32_t kPolicyThreads = 1024;
+constexpr uint32_t kPolicyAlone = 2;   // turns that one workgroup takes sooner than joining sums
 constexpr uint32_t kPolicySums = 5;   // loss, weight, kl, clipped, entropy
 struct PolicyArgs {
     const float *logp, *old, *advantages, *weights, *ref, *entropy;
@@ -79,6 +85,8 @@ hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream);
 // ones, and fewer additions to the shared sums at the end.
 constexpr uint32_t kBalanceGrid = 256;
 constexpr uint32_t kBalanceThreads = 1024;
+constexpr uint32_t kBalanceAlone = 4;        // turns that one takes sooner than joining sums
+constexpr uint32_t kBalanceCopies = 8;       // of the sums that workgroups add to
 constexpr uint32_t kBalanceGradGrid = 2048;   // of four waves
 struct BalanceArgs {
     const void *logits, *chosen;
@@ -88,7 +96,7 @@ struct BalanceArgs {
     double balance_coef, z_coef;
     int64_t *counts;
     bf16d_balance_result *result;
-    uint64_t *sums;      // kBalanceWords accumulators, zero between calls
+    uint64_t *sums;      // kBalanceCopies times 2 * experts + 3, zero between calls
     uint64_t *partial;   // a workgroup's sum of squares
     uint32_t *done;
 };
@@ -111,9 +119,14 @@ typedef uint32_t word4 __attribute__((ext_vector_type(4)));
 // 16 bytes at an address of a 2- or 4-byte type's alignment
 typedef word4 word4_any __attribute__((aligned(2)));
 
+// a / b of uniform numbers, as one: there is no scalar division, and the quotient would
+// stay in vector registers, with all that is computed from it
+__device__ __forceinline__ uint32_t scalar_div(uint32_t a, uint32_t b) {
+    return b == 1 ? a : first_lane(a / b);
+}
 __device__ __forceinline__ const uint8_t *row_ptr(const RowSet &s, uint32_t row, uint32_t inner,
                                                   uint32_t size) {
-    const uint32_t o = row / inner, i = row - o * inner;
+    const uint32_t o = scalar_div(row, inner), i = row - o * inner;
     return static_cast<const uint8_t *>(s.data) +
            (o * s.outer_stride + i * s.inner_stride) * size;
 }
@@ -176,6 +189,31 @@ __device__ __forceinline__ void both_halves(double v, double &even, double &odd)
     even = __longlong_as_double((long long)((uint64_t)hi[0] << 32 | lo[0]));
     odd = __longlong_as_double((long long)((uint64_t)hi[1] << 32 | lo[1]));
 }
+// v of the lane whose number differs in the bits of kMask
+template <int kMask>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+    constexpr int kLow = kMask & 15;
+    static_assert(kLow == 0 || kLow == 1 || kLow == 2 || kLow == 3 || kLow == 4 || kLow == 7 ||
+                      kLow == 8 || kLow == 15,
+                  "one or two moves within a row of 16 lanes");
+    if constexpr (kLow == 1) v = dpp_src<0xB1>(v);
+    if constexpr (kLow == 2) v = dpp_src<0x4E>(v);
+    if constexpr (kLow == 3) v = dpp_src<0x1B>(v);                   // quad_perm 3 2 1 0
+    if constexpr (kLow == 4) v = dpp_src<0x1B>(dpp_src<0x141>(v));   // 7, then 3
+    if constexpr (kLow == 7) v = dpp_src<0x141>(v);
+    if constexpr (kLow == 8) v = dpp_src<0x128>(v);                  // row_ror:8
+    if constexpr (kLow == 15) v = dpp_src<0x140>(v);
+    if constexpr ((kMask & 16) != 0) {
+        auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = threadIdx.x & 16 ? r[0] : r[1];
+    }
+    if constexpr ((kMask & 32) != 0) {
+        auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = threadIdx.x & 32 ? r[0] : r[1];
+    }
+    return v;
+}
+
 template <typename Op, typename T>
 __device__ __forceinline__ T lanes_reduce(T v, uint32_t lanes = 64) {
     const Op op;

@@ -60,25 +60,30 @@ bool count_rows(uint64_t outer, uint64_t inner, uint64_t &rows) {
            inner < kMaxRows;
 }
 
-// Workgroups of a row: enough for kLogprobGroups in all, at most one for each turn.
-uint32_t parts_of(uint64_t rows, uint32_t turns) {
-    const uint64_t wanted = (kLogprobGroups + rows - 1) / rows;
-    const uint64_t parts = std::min<uint64_t>(wanted, turns);
-    // whole turns each: fewer parts may do
-    const uint64_t each = (turns + parts - 1) / parts;
-    return uint32_t((turns + each - 1) / each);
+// How rows are cut: into `parts` workgroups each, enough for `groups` in all, of
+// part_turns turns.
+struct Cut {
+    uint32_t parts, part_turns;
+};
+Cut cut_rows(uint64_t rows, uint32_t turns, uint32_t groups) {
+    const uint64_t wanted = (groups + rows - 1) / rows;
+    const uint32_t parts = uint32_t(std::min<uint64_t>(wanted, turns));
+    const uint32_t each = (turns + parts - 1) / parts;
+    return Cut{(turns + each - 1) / each, each};   // whole turns each: fewer parts may do
 }
 
-// counters (rows in parts are fewer than kLogprobGroups), then the parts' words
-constexpr size_t kCounterBytes = 4 * size_t(kLogprobGroups);
+// counters (rows in parts are fewer than the workgroups), then the parts' words
+constexpr uint32_t kMostGroups = std::max(kLogprobGroups, kLogprobWideGroups);
+constexpr size_t kCounterBytes = 4 * size_t(kMostGroups);
 size_t logprob_workspace(uint64_t rows, uint32_t turns, uint32_t top) {
     if (rows == 0 || turns <= 1) return 0;
-    // rows * ceil(groups / rows) is below groups + rows, and nothing is cut
-    // from `groups` rows on
-    const uint64_t cut = std::min<uint64_t>(rows, kLogprobGroups - 1);
-    const uint64_t words = std::min<uint64_t>(cut * turns, kLogprobGroups + cut) * (2 + top);
+    // rows * ceil(groups / rows) is below groups + rows, and nothing is cut from
+    // `groups` rows on
+    const uint64_t cut = std::min<uint64_t>(rows, kMostGroups - 1);
+    const uint64_t words = std::min<uint64_t>(cut * turns, kMostGroups + cut) * (2 + top);
     return kCounterBytes + 8 * words;
 }
+static_assert(kLogprobWide >= kThreads, "turns of wide workgroups are fewer");
 
 bool finite(double x) { return std::isfinite(x); }
 
@@ -97,8 +102,8 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
         !aligned(J.tokens.data, id_size(J.token_dtype)))
         return BF16D_EINVAL;
     const uint64_t size = logits_size(J.logits_dtype);
-    const uint32_t turns = turns_of(J.vocab, J.logits_dtype,
-                                    rows_aligned(J.logits, J.outer, J.inner, size));
+    const bool at16 = rows_aligned(J.logits, J.outer, J.inner, size);
+    const uint32_t turns = turns_of(J.vocab, J.logits_dtype, at16, kThreads);
     if (rows > 0) {
         if (!J.logits.data || !J.tokens.data || !J.logp) return BF16D_EINVAL;
         if ((J.top > 0) != (J.top_ids != nullptr) || (J.top > 0) != (J.top_logp != nullptr))
@@ -131,8 +136,14 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     a.vocab = J.vocab;
     a.token_i32 = J.token_dtype == BF16D_IDS_I32;
     a.top = J.top;
-    a.parts = parts_of(rows, turns);
-    a.part_turns = (turns + a.parts - 1) / a.parts;
+    // wide: with alternatives, and where that is one turn of a workgroup, and the
+    // workgroups one for each CU
+    const uint32_t wide_turns = turns_of(J.vocab, J.logits_dtype, at16, kLogprobWide);
+    const bool wide = J.top > 0 || (turns > 1 && wide_turns == 1 && rows <= kLogprobGroups);
+    const Cut cut = wide ? cut_rows(rows, wide_turns, kLogprobWideGroups)
+                         : cut_rows(rows, turns, kLogprobGroups);
+    a.parts = cut.parts;
+    a.part_turns = cut.part_turns;
     const bool keep = J.stats && rows * J.vocab * size <= kLogprobKept;
     a.scale = float(1.4426950408889634 / J.temperature);
     a.inv_t = float(1.0 / J.temperature);
@@ -143,7 +154,7 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     a.top_logp = J.top_logp;
     a.done = static_cast<uint32_t *>(workspace);
     a.partial = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
-    return launch_logprob(a, J.logits_dtype == BF16D_LOGITS_F32, keep, stream) == hipSuccess
+    return launch_logprob(a, J.logits_dtype == BF16D_LOGITS_F32, wide, keep, stream) == hipSuccess
                ? BF16D_OK
                : BF16D_EHIP;
 }
@@ -187,7 +198,7 @@ int logprob_backward(const bf16d_logprob_grad_job *job, hipStream_t stream) {
     const int rc = stream_on_current(stream, dev);
     if (rc != BF16D_OK || rows == 0) return rc;
     const uint32_t turns = turns_of(J.vocab, J.logits_dtype,
-                                    rows_aligned(J.logits, J.outer, J.inner, size));
+                                    rows_aligned(J.logits, J.outer, J.inner, size), kThreads);
     LogprobGradArgs a{};
     a.logits = row_set(J.logits);
     a.tokens = row_set(J.tokens);
@@ -262,13 +273,13 @@ int policy_loss(const bf16d_policy_job *job, bf16d_policy_result *result, void *
     return launch_policy_loss(a, stream) == hipSuccess ? BF16D_OK : BF16D_EHIP;
 }
 
-// accumulators (counts, sums of p, three more), partial sums, the counter
+// accumulators (counts, sums of p, three more; in copies), partial sums, the counter
 struct BalanceSpace {
     size_t partial, done, total;
 };
 BalanceSpace balance_space(uint32_t experts) {
     BalanceSpace s;
-    s.partial = align_up(8 * (2 * size_t(experts) + 3), 16);
+    s.partial = align_up(8 * kBalanceCopies * (2 * size_t(experts) + 3), 16);
     s.done = s.partial + 8 * size_t(kBalanceGrid);
     s.total = s.done + 16;
     return s;
@@ -405,7 +416,8 @@ extern "C" {
 size_t bf16d_logprob_workspace_bytes(uint64_t rows, uint32_t vocab, uint32_t top) {
     if (vocab == 0) return 0;
     // fp32 rows have more turns
-    const uint32_t turns = turns_of(std::min(vocab, BF16D_MAX_VOCAB), BF16D_LOGITS_F32, false);
+    const uint32_t turns =
+        turns_of(std::min(vocab, BF16D_MAX_VOCAB), BF16D_LOGITS_F32, false, kThreads);
     return logprob_workspace(rows, turns, std::min(top, BF16D_MAX_TOP));
 }
 

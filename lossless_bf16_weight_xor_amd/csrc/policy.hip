@@ -135,8 +135,9 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_loss_kernel(PolicyArgs 
 }  // namespace
 
 hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream) {
-    const uint64_t groups = (a.n + kPolicyThreads - 1) / kPolicyThreads;
-    const uint32_t grid = groups < kPolicyGrid ? (groups ? (uint32_t)groups : 1) : kPolicyGrid;
+    const uint64_t turns = (a.n + kPolicyThreads - 1) / kPolicyThreads;
+    const uint32_t grid =
+        turns <= kPolicyAlone ? 1 : turns < kPolicyGrid ? (uint32_t)turns : kPolicyGrid;
     return launch_one(policy_loss_kernel, grid, kPolicyThreads, a, 0, stream);
 }
 

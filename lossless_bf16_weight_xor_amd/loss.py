@@ -20,6 +20,7 @@ Tensors that are passed in stay their owner's, as in any torch call.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -29,11 +30,20 @@ from .step import _raw_stream
 
 _LOGITS = {torch.bfloat16: _native.LOGITS_BF16, torch.float32: _native.LOGITS_F32}
 _IDS = {torch.int64: _native.IDS_I64, torch.int32: _native.IDS_I32}
+_F32 = (torch.float32,)
 _BYTES = (torch.bool, torch.uint8)
 _MAX_ROWS = (1 << 24) - 1
+# The parts of the jobs that a call fills in, packed at once: 0.5 us, where a field
+# at a time takes 1 of a call's 6.
+_LOGPROB = struct.Struct("8Q4Id").pack_into
+_LOGPROB_GRAD = struct.Struct("11Q4I3Q").pack_into
+_POLICY = struct.Struct("9Q5d").pack_into
+_BALANCE = struct.Struct("6Q4I").pack_into
+_BALANCE_GRAD = struct.Struct("6Q2I3d").pack_into
 
 
 def _refuse(t, what: str, dtypes, shape, device) -> None:
+    """Says what is wrong with a tensor that a call did not take."""
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise TypeError(f"{what} must be a tensor on a HIP device (got "
                         f"{getattr(t, 'device', type(t))}); there is no CPU path")
@@ -41,36 +51,22 @@ def _refuse(t, what: str, dtypes, shape, device) -> None:
         raise TypeError(f"{what} must be of type {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{what}: the elements of a row must be adjacent")
-
-
-def _table(t, what: str, dtypes, device, width: int | None) -> None:
-    """A tensor of rows of `width` adjacent elements (None: of any width)."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index
-            and t.dtype in dtypes):
-        _refuse(t, what, dtypes, None, device)
-    if t.dim() < 1 or (width is not None and t.shape[-1] != width):
-        raise ValueError(f"{what} must have rows of {width} elements, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
-        _refuse(t, what, dtypes, None, device)
+    if len(t.shape) != len(shape) or any(a is not None and a != b
+                                         for a, b in zip(shape, t.shape)):
+        wanted = ", ".join("any" if a is None else str(a) for a in shape)
+        raise ValueError(f"{what} must have the shape ({wanted}), got {tuple(t.shape)}")
+    raise ValueError(f"{what}: the elements of a row must be adjacent, got strides {t.stride()}")
 
 
 def _row(t, what: str, dtypes, n: int, device) -> int:
-    """The address of n adjacent elements."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index
+    """The address of n adjacent elements of any shape."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == device.index
             and t.dtype in dtypes):
-        _refuse(t, what, dtypes, None, device)
+        _refuse(t, what, dtypes, (None,), device)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must hold {n} elements, contiguous; got {tuple(t.shape)} with "
                          f"strides {t.stride()}")
     return t.data_ptr()
-
-
-def _two_levels(t: torch.Tensor, dims: int) -> tuple[int, int]:
-    """The strides of a tensor's first `dims` dimensions (1 or 2), outer and inner."""
-    return (0, t.stride(0)) if dims == 1 else (t.stride(0), t.stride(1))
 
 
 class _Op:
@@ -119,7 +115,7 @@ class _Op:
                 for t in self._buffers:
                     t.record_stream(s)
 
-    def _call(self, fn, what: str, *args) -> None:
+    def _call(self, fn, what: str, args) -> None:
         """fn(*args, stream) on the current stream of the operator's device."""
         stream = _raw_stream(self._index)
         if stream != self._stream0:
@@ -129,7 +125,8 @@ class _Op:
         else:
             with torch.cuda.device(self.device):
                 rc = fn(*args, stream)
-        _check_rc(rc, what)
+        if rc:
+            _check_rc(rc, what)
 
 
 class TokenLogProbs(_Op):
@@ -169,31 +166,39 @@ class TokenLogProbs(_Op):
         self._ready()
         self._ran = None    # rows of the last run
         at = lambda t: t.data_ptr() if t is not None else None
-        self._job = _native.LogprobJob(vocab=self.vocab, top=self.top, logp=at(self.logp),
-                                       entropy=at(self.entropy), stats=at(self.stats),
-                                       top_ids=at(self.top_ids), top_logp=at(self.top_logp))
+        self._job = _native.LogprobJob(logp=at(self.logp), entropy=at(self.entropy),
+                                       stats=at(self.stats), top_ids=at(self.top_ids),
+                                       top_logp=at(self.top_logp))
+        self._fn = self._lib.bf16d_logprob
         self._args = (ctypes.byref(self._job), self._workspace.data_ptr(), size)
-        self._grad_job = _native.LogprobGradJob(vocab=self.vocab, stats=self.stats.data_ptr())
+        self._stats = self.stats.data_ptr()
+        self._grad_job = _native.LogprobGradJob()
+        self._grad_fn = self._lib.bf16d_logprob_backward
         self._grad_args = (ctypes.byref(self._grad_job),)
 
-    def _rows_of(self, job, logits, tokens) -> int:
-        """Fills in the logits and tokens of a call and returns its number of rows."""
-        _table(logits, "logits", _LOGITS, self.device, self.vocab)
-        dims = logits.dim() - 1
-        if dims not in (1, 2):
+    def _rows_of(self, logits, tokens) -> tuple:
+        """(rows; address and strides of the logits, of the tokens, outer, inner)."""
+        if not (isinstance(logits, torch.Tensor) and logits.get_device() == self._index
+                and logits.dtype in _LOGITS):
+            _refuse(logits, "logits", _LOGITS, (None, self.vocab), self.device)
+        shape, strides = logits.shape, logits.stride()
+        if len(shape) not in (2, 3):
             raise ValueError(f"logits must be (rows, vocab) or (batch, length, vocab), got "
-                             f"{tuple(logits.shape)}")
-        if not (isinstance(tokens, torch.Tensor) and tokens.is_cuda
-                and tokens.get_device() == self._index and tokens.dtype in _IDS
-                and tokens.shape == logits.shape[:-1]):
-            _refuse(tokens, "tokens", _IDS, logits.shape[:-1], self.device)
-        job.outer, job.inner = (1, logits.shape[0]) if dims == 1 else logits.shape[:2]
-        job.logits = logits.data_ptr()
-        job.logits_outer, job.logits_inner = _two_levels(logits, dims)
-        job.tokens = tokens.data_ptr()
-        job.tokens_outer, job.tokens_inner = _two_levels(tokens, dims)
-        job.logits_dtype, job.token_dtype = _LOGITS[logits.dtype], _IDS[tokens.dtype]
-        return self._count(job.outer * job.inner)
+                             f"{tuple(shape)}")
+        rows = shape[:-1]
+        if shape[-1] != self.vocab or (strides[-1] != 1 and self.vocab > 1 and logits.numel()):
+            _refuse(logits, "logits", _LOGITS, (*rows, self.vocab), self.device)
+        if not (isinstance(tokens, torch.Tensor) and tokens.get_device() == self._index
+                and tokens.dtype in _IDS and tokens.shape == rows):
+            _refuse(tokens, "tokens", _IDS, rows, self.device)
+        if len(shape) == 2:
+            outer, inner = 1, shape[0]
+            t_outer, (t_inner,), l_outer = 0, tokens.stride(), 0
+        else:
+            outer, inner = rows
+            (t_outer, t_inner), l_outer = tokens.stride(), strides[0]
+        return (self._count(outer * inner), logits.data_ptr(), l_outer, strides[-2],
+                tokens.data_ptr(), t_outer, t_inner, outer, inner)
 
     def run(self, logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0) -> None:
         """logits: bf16 or fp32, (rows, vocab) or (batch, length, vocab), a row's
@@ -202,9 +207,10 @@ class TokenLogProbs(_Op):
         by, from 2^-20 to 2^20."""
         if not 2.0 ** -20 <= temperature <= 2.0 ** 20:
             raise ValueError(f"temperature must be from 2^-20 to 2^20, got {temperature}")
-        n = self._rows_of(self._job, logits, tokens)
-        self._job.temperature = temperature
-        self._call(self._lib.bf16d_logprob, "bf16d_logprob", *self._args)
+        n, *rows = self._rows_of(logits, tokens)
+        _LOGPROB(self._job, 0, *rows, self.vocab, _LOGITS[logits.dtype], _IDS[tokens.dtype],
+                 self.top, temperature)
+        self._call(self._fn, "bf16d_logprob", self._args)
         self._ran = n
 
     def backward(self, logits: torch.Tensor, tokens: torch.Tensor, grad_logp: torch.Tensor,
@@ -212,24 +218,26 @@ class TokenLogProbs(_Op):
         """The gradient of sum(grad_logp * logp + grad_entropy * entropy) by the logits, into
         `out` (their type and shape; the logits themselves are fine).  logits and
         tokens: those of the last run; grad_logp, grad_entropy: float32, one a row."""
-        job = self._grad_job
-        n = self._rows_of(job, logits, tokens)
+        n, *rows = self._rows_of(logits, tokens)
         if n != self._ran:
             raise ValueError(f"{n} rows, but the last run had {self._ran}: backward needs its "
                              f"softmax sums")
-        _table(out, "out", (logits.dtype,), self.device, self.vocab)
-        if out.shape != logits.shape:
-            raise ValueError(f"out must have the logits' shape {tuple(logits.shape)}, got "
-                             f"{tuple(out.shape)}")
-        job.out = out.data_ptr()
-        job.out_outer, job.out_inner = _two_levels(out, logits.dim() - 1)
-        job.grad_logp = _row(grad_logp, "grad_logp", (torch.float32,), n, self.device)
-        job.grad_entropy = None
+        kind = logits.dtype
+        if not (isinstance(out, torch.Tensor) and out.get_device() == self._index
+                and out.dtype == kind and out.shape == logits.shape
+                and (out.stride(-1) == 1 or self.vocab == 1 or not n)):
+            _refuse(out, "out", (kind,), logits.shape, self.device)
+        strides = out.stride()
+        a = _row(grad_logp, "grad_logp", _F32, n, self.device)
+        h = 0
         if grad_entropy is not None:
             if self.entropy is None:
                 raise ValueError("grad_entropy needs an operator prepared with entropy=True")
-            job.grad_entropy = _row(grad_entropy, "grad_entropy", (torch.float32,), n, self.device)
-        self._call(self._lib.bf16d_logprob_backward, "bf16d_logprob_backward", *self._grad_args)
+            h = _row(grad_entropy, "grad_entropy", _F32, n, self.device)
+        _LOGPROB_GRAD(self._grad_job, 0, *rows[:6], out.data_ptr(),
+                      strides[0] if len(strides) == 3 else 0, strides[-2], *rows[6:], self.vocab,
+                      _LOGITS[kind], _IDS[tokens.dtype], 0, self._stats, a, h)
+        self._call(self._grad_fn, "bf16d_logprob_backward", self._grad_args)
 
 
 class PolicyLoss(_Op):
@@ -253,9 +261,11 @@ class PolicyLoss(_Op):
         size = int(self._lib.bf16d_policy_loss_workspace_bytes())
         self._workspace = self._zeros(size, torch.uint8)
         self._ready()
-        self._job = _native.PolicyJob(grad_logp=self.grad_logp.data_ptr())
+        self._job = _native.PolicyJob()
+        self._fn = self._lib.bf16d_policy_loss
         self._args = (ctypes.byref(self._job), self.result.data_ptr(),
                       self._workspace.data_ptr(), size)
+        self._grads = self.grad_logp.data_ptr(), self.grad_entropy.data_ptr()
 
     def run(self, logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
             weights: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None,
@@ -269,23 +279,22 @@ class PolicyLoss(_Op):
         entropy  : of the policy, for entropy_coef and the mean
         clip     : how far a ratio counts below and above 1 (infinity above: no bound)
         scale    : of the loss and the gradients, 1 / the batch's tokens for example"""
-        job, f32 = self._job, (torch.float32,)
-        n = self._count(logp.numel() if isinstance(logp, torch.Tensor) else 0)
-        job.n = n
-        job.logp = _row(logp, "logp", f32, n, self.device)
-        job.old = _row(old_logp, "old_logp", f32, n, self.device)
-        job.advantages = _row(advantages, "advantages", f32, n, self.device)
-        job.weights = None if weights is None else _row(weights, "weights", f32, n, self.device)
-        job.ref = None if ref_logp is None else _row(ref_logp, "ref_logp", f32, n, self.device)
-        job.entropy = job.grad_entropy = None
-        if entropy is not None:
-            job.entropy = _row(entropy, "entropy", f32, n, self.device)
-            job.grad_entropy = self.grad_entropy.data_ptr()
+        if not isinstance(logp, torch.Tensor):
+            _refuse(logp, "logp", _F32, (None,), self.device)
+        n, device = self._count(logp.numel()), self.device
         if (kl_coef != 0.0 and ref_logp is None) or (entropy_coef != 0.0 and entropy is None):
             raise ValueError("kl_coef needs ref_logp, and entropy_coef needs entropy")
-        job.clip_low, job.clip_high = clip
-        job.kl_coef, job.entropy_coef, job.scale = kl_coef, entropy_coef, scale
-        self._call(self._lib.bf16d_policy_loss, "bf16d_policy_loss", *self._args)
+        low, high = clip
+        grad_logp, grad_entropy = self._grads
+        _POLICY(self._job, 0, _row(logp, "logp", _F32, n, device),
+                _row(old_logp, "old_logp", _F32, n, device),
+                _row(advantages, "advantages", _F32, n, device),
+                0 if weights is None else _row(weights, "weights", _F32, n, device),
+                0 if ref_logp is None else _row(ref_logp, "ref_logp", _F32, n, device),
+                0 if entropy is None else _row(entropy, "entropy", _F32, n, device),
+                grad_logp, 0 if entropy is None else grad_entropy, n, low, high, kl_coef,
+                entropy_coef, scale)
+        self._call(self._fn, "bf16d_policy_loss", self._args)
 
 
 class RouterBalance(_Op):
@@ -319,52 +328,63 @@ class RouterBalance(_Op):
         self._workspace = self._zeros(size, torch.uint8)
         self._ready()
         self._ran = False
-        coefs = dict(balance_coef=balance_coef, z_coef=z_coef)
-        self._job = _native.BalanceJob(experts=self.experts, counts=self.counts.data_ptr(), **coefs)
+        self._coefs = float(balance_coef), float(z_coef)
+        self._job = _native.BalanceJob(balance_coef=balance_coef, z_coef=z_coef,
+                                       counts=self.counts.data_ptr())
+        self._fn = self._lib.bf16d_balance
         self._args = (ctypes.byref(self._job), self.result.data_ptr(),
                       self._workspace.data_ptr(), size)
-        self._grad_job = _native.BalanceGradJob(
-            experts=self.experts, counts=self.counts.data_ptr(), tokens=self.tokens.data_ptr(),
-            result=self.result.data_ptr(), **coefs)
+        self._grad_job = _native.BalanceGradJob(counts=self.counts.data_ptr(),
+                                                tokens=self.tokens.data_ptr(),
+                                                result=self.result.data_ptr())
+        self._grad_fn = self._lib.bf16d_balance_backward
         self._grad_args = (ctypes.byref(self._grad_job),)
 
-    def _rows_of(self, job, logits, mask) -> int:
-        _table(logits, "logits", _LOGITS, self.device, self.experts)
-        if logits.dim() != 2:
-            raise ValueError(f"logits must be (tokens, experts), got {tuple(logits.shape)}")
-        n = self._count(logits.shape[0])
-        job.rows, job.logits, job.logits_stride = n, logits.data_ptr(), logits.stride(0)
-        job.logits_dtype = _LOGITS[logits.dtype]
-        job.mask = None if mask is None else _row(mask, "mask", _BYTES, n, self.device)
-        return n
+    def _rows_of(self, logits, mask) -> tuple:
+        """(rows, row stride, address of the mask)"""
+        if not (isinstance(logits, torch.Tensor) and logits.get_device() == self._index
+                and logits.dtype in _LOGITS and logits.dim() == 2):
+            _refuse(logits, "logits", _LOGITS, (None, self.experts), self.device)
+        n, experts = logits.shape
+        stride, step = logits.stride()
+        if experts != self.experts or (step != 1 and experts > 1 and n):
+            _refuse(logits, "logits", _LOGITS, (None, self.experts), self.device)
+        return (self._count(n), stride,
+                0 if mask is None else _row(mask, "mask", _BYTES, n, self.device))
 
     def run(self, logits: torch.Tensor, chosen: torch.Tensor,
             mask: torch.Tensor | None = None) -> None:
         """logits: bf16 or fp32, (tokens, experts).  chosen: int64 or int32, (tokens,
         choices), the ids of each token's experts (a negative one is no choice).
         mask: bool or uint8, which tokens count; None: all."""
-        job = self._job
-        n = self._rows_of(job, logits, mask)
-        _table(chosen, "chosen", _IDS, self.device, None)
-        if chosen.dim() != 2 or chosen.shape[0] != n or not 1 <= chosen.shape[1] <= self.experts:
-            raise ValueError(f"chosen must be (tokens, choices) for {n} tokens and at most "
-                             f"{self.experts} choices, got {tuple(chosen.shape)}")
-        job.chosen, job.chosen_stride = chosen.data_ptr(), chosen.stride(0)
-        job.choices, job.chosen_dtype = chosen.shape[1], _IDS[chosen.dtype]
-        self._call(self._lib.bf16d_balance, "bf16d_balance", *self._args)
+        n, stride, seen = self._rows_of(logits, mask)
+        if not (isinstance(chosen, torch.Tensor) and chosen.get_device() == self._index
+                and chosen.dtype in _IDS and chosen.dim() == 2 and chosen.shape[0] == n):
+            _refuse(chosen, "chosen", _IDS, (n, None), self.device)
+        choices = chosen.shape[1]
+        if not 1 <= choices <= self.experts:
+            raise ValueError(f"chosen must name from 1 to {self.experts} experts a token, got "
+                             f"{choices}")
+        chosen_stride, step = chosen.stride()
+        if step != 1 and choices > 1 and n:
+            _refuse(chosen, "chosen", _IDS, (n, None), self.device)
+        _BALANCE(self._job, 0, logits.data_ptr(), chosen.data_ptr(), seen, n, stride,
+                 chosen_stride, self.experts, choices, _LOGITS[logits.dtype], _IDS[chosen.dtype])
+        self._call(self._fn, "bf16d_balance", self._args)
         self._ran = True
 
     def backward(self, logits: torch.Tensor, out: torch.Tensor, mask: torch.Tensor | None = None,
                  scale: float = 1.0) -> None:
         """scale * the gradient of the loss by the logits, into `out` (their type and shape;
         the logits themselves are fine).  logits, mask: those of the last run."""
-        job = self._grad_job
         if not self._ran:
             raise ValueError("backward needs the counts of a run")
-        self._rows_of(job, logits, mask)
-        _table(out, "out", (logits.dtype,), self.device, self.experts)
-        if out.shape != logits.shape:
-            raise ValueError(f"out must have the logits' shape {tuple(logits.shape)}, got "
-                             f"{tuple(out.shape)}")
-        job.out, job.out_stride, job.scale = out.data_ptr(), out.stride(0), scale
-        self._call(self._lib.bf16d_balance_backward, "bf16d_balance_backward", *self._grad_args)
+        n, stride, seen = self._rows_of(logits, mask)
+        kind = logits.dtype
+        if not (isinstance(out, torch.Tensor) and out.get_device() == self._index
+                and out.dtype == kind and out.shape == logits.shape
+                and (out.stride(1) == 1 or self.experts == 1 or not n)):
+            _refuse(out, "out", (kind,), logits.shape, self.device)
+        _BALANCE_GRAD(self._grad_job, 0, logits.data_ptr(), out.data_ptr(), seen, n, stride,
+                      out.stride(0), self.experts, _LOGITS[kind], *self._coefs, scale)
+        self._call(self._grad_fn, "bf16d_balance_backward", self._grad_args)

@@ -95,8 +95,8 @@ def test_logprob_refuses_a_short_workspace(native):
     # 4 rows of 5 turns each
     wide = dict(vocab=40000, logits_inner=40000)
     need = native.lib().bf16d_logprob_workspace_bytes(4, 40000, 3)
-    assert need >= 4 * 1024 + 4 * 5 * 5 * 8
-    assert _logprob(native, size=4 * 1024 + 4 * 5 * 5 * 8 - 8, **wide) == E
+    assert need >= 4 * 512 + 4 * 5 * 5 * 8
+    assert _logprob(native, size=4 * 512 + 4 * 5 * 5 * 8 - 8, **wide) == E
     assert _logprob(native, workspace=None, **wide) == E
     assert _logprob(native, workspace=_at(9) + 8, **wide) == E
     assert _logprob(native, workspace=_at(2), **wide) == E        # over an output
@@ -266,16 +266,16 @@ def test_balance_backward_refusals(native):
 def test_workspaces_grow_with_the_call(native):
     f = native.lib().bf16d_logprob_workspace_bytes
     assert f(0, 100000, 5) == 0 and f(100, 0, 0) == 0
-    assert f(100, 4096, 5) == 0                      # one turn: nothing to join
+    assert f(100, 4093, 5) == 0             # one turn at any alignment: nothing to join
     assert 0 < f(1, 100000, 0) < f(1, 100000, 5) <= f(2, 100000, 5) <= f(10 ** 6, 100000, 5)
     assert f(10 ** 6, 1 << 28, 64) < 2 << 20
     # what a call of fewer rows needs is never more: rows * parts, for every number of rows
     for turns in (2, 3, 7, 33, 5000):
         vocab = turns * 4096
         for rows in (1, 2, 3, 5, 31, 100, 500, 1000, 1023, 1024, 5000):
-            words = (f(rows, vocab, 3) - 4096) // 8
+            words = (f(rows, vocab, 3) - 2048) // 8
             for fewer in {k for k in (1, 2, rows // 2, rows - 1, rows) if 0 < k <= rows}:
-                parts = min(-(-1024 // fewer), turns)
+                parts = min(-(-512 // fewer), turns)
                 if parts > 1:
                     assert words >= fewer * parts * 5, (turns, rows, fewer)
     g = native.lib().bf16d_balance_workspace_bytes
