@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
             dep ^= __hip_atomic_exchange(a.partial + blockIdx.x,
                                          (uint64_t)__double_as_longlong(x[0]), __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT);
-        if (!last_of(a.done, gridDim.x, dep)) return;
+        if (!last_of_launch(a.done, dep)) return;
         clear();
         // the copies are read and cleared
         const uint32_t copies = gridDim.x < kBalanceCopies ? gridDim.x : kBalanceCopies;
@@ -265,8 +265,6 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         a.result->z = (float)z;
         a.result->loss = (float)(a.balance_coef * balance + a.z_coef * z);
         a.result->tokens = (int64_t)n;
-        if (gridDim.x > 1)
-            __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 

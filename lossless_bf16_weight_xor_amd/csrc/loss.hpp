@@ -76,7 +76,7 @@ struct PolicyArgs {
     double kl_coef, entropy_coef, scale;
     bf16d_policy_result *result;
     uint64_t *partial;             // kPolicySums words a workgroup
-    uint32_t *done;
+    uint32_t *done;                // kDoneWords
 };
 hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream);
 
@@ -98,7 +98,7 @@ struct BalanceArgs {
     bf16d_balance_result *result;
     uint64_t *sums;      // kBalanceCopies times 2 * experts + 3, zero between calls
     uint64_t *partial;   // a workgroup's sum of squares
-    uint32_t *done;
+    uint32_t *done;      // kDoneWords
 };
 hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream);
 
@@ -143,6 +143,34 @@ __device__ __forceinline__ bool last_of(uint32_t *done, uint32_t count, uint64_t
     if (threadIdx.x == 0)
         s_last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                  count - 1;
+    __syncthreads();
+    return s_last;
+}
+
+// The same for all workgroups of a launch, in two levels: additions to one address
+// take 20 ns each, 5 us for 256 workgroups.  done: kDoneWords counters.
+constexpr uint32_t kDoneGroups = 16, kDoneStride = 32;   // words: a line each
+constexpr uint32_t kDoneWords = (kDoneGroups + 1) * kDoneStride;
+__device__ __forceinline__ bool last_of_launch(uint32_t *done, uint64_t dep) {
+    __shared__ bool s_last;
+    asm volatile("" ::"v"(dep) : "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        auto arrive = [&](uint32_t *at, uint32_t count) {
+            const bool last = __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT) == count - 1;
+            if (last) __hip_atomic_store(at, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            return last;
+        };
+        uint32_t *all = done + kDoneGroups * kDoneStride;
+        const uint32_t group = blockIdx.x % kDoneGroups;
+        if (gridDim.x <= kDoneGroups)
+            s_last = arrive(all, gridDim.x);
+        else
+            s_last = arrive(done + group * kDoneStride,
+                            (gridDim.x - group + kDoneGroups - 1) / kDoneGroups) &&
+                     arrive(all, kDoneGroups);
+    }
     __syncthreads();
     return s_last;
 }

@@ -219,7 +219,7 @@ int logprob_backward(const bf16d_logprob_grad_job *job, hipStream_t stream) {
                : BF16D_EHIP;
 }
 
-// partial sums, then the counter
+// partial sums, then the counters
 constexpr size_t kPolicyPartial = 8 * size_t(kPolicyGrid) * kPolicySums;
 
 int policy_loss(const bf16d_policy_job *job, bf16d_policy_result *result, void *workspace,
@@ -273,7 +273,7 @@ int policy_loss(const bf16d_policy_job *job, bf16d_policy_result *result, void *
     return launch_policy_loss(a, stream) == hipSuccess ? BF16D_OK : BF16D_EHIP;
 }
 
-// accumulators (counts, sums of p, three more; in copies), partial sums, the counter
+// accumulators (counts, sums of p, three more; in copies), partial sums, the counters
 struct BalanceSpace {
     size_t partial, done, total;
 };
@@ -281,7 +281,7 @@ BalanceSpace balance_space(uint32_t experts) {
     BalanceSpace s;
     s.partial = align_up(8 * kBalanceCopies * (2 * size_t(experts) + 3), 16);
     s.done = s.partial + 8 * size_t(kBalanceGrid);
-    s.total = s.done + 16;
+    s.total = s.done + 4 * kDoneWords;
     return s;
 }
 
@@ -430,7 +430,7 @@ int bf16d_logprob_backward(const bf16d_logprob_grad_job *job, hipStream_t stream
     return guarded([&] { return logprob_backward(job, stream); });
 }
 
-size_t bf16d_policy_loss_workspace_bytes(void) { return kPolicyPartial + 16; }
+size_t bf16d_policy_loss_workspace_bytes(void) { return kPolicyPartial + 4 * kDoneWords; }
 
 int bf16d_policy_loss(const bf16d_policy_job *job, bf16d_policy_result *result, void *workspace,
                       size_t workspace_bytes, hipStream_t stream) {

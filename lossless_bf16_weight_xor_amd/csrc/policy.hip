@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_loss_kernel(PolicyArgs 
     }
     group_sums(sum, s_tmp);
     if (gridDim.x > 1) {
-        // handed over by returning device-scope atomics, as last_of asks
+        // handed over by returning device-scope atomics, as last_of_launch asks
         uint64_t dep = 0;
         if (threadIdx.x < kPolicySums) {
             double mine = sum[0];
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_loss_kernel(PolicyArgs 
                                         (uint64_t)__double_as_longlong(mine), __ATOMIC_RELAXED,
                                         __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (!last_of(a.done, gridDim.x, dep)) return;
+        if (!last_of_launch(a.done, dep)) return;
         static_assert(kPolicyGrid <= kPolicyThreads, "a thread takes one workgroup's sums");
 #pragma unroll
         for (uint32_t k = 0; k < kPolicySums; ++k)
@@ -127,8 +127,6 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_loss_kernel(PolicyArgs 
         a.result->kl = (float)(sum[2] * over);
         a.result->clipped = (float)(sum[3] * over);
         a.result->entropy = (float)(sum[4] * over);
-        if (gridDim.x > 1)
-            __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 

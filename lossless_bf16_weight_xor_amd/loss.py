@@ -20,6 +20,8 @@ Tensors that are passed in stay their owner's, as in any torch call.
 from __future__ import annotations
 
 import ctypes
+import itertools
+import math
 import struct
 
 import torch
@@ -84,22 +86,22 @@ class _Op:
         self.device = device
         self._index = device.index
         self._lib = _native.lib()
-        self._buffers = []
         with torch.cuda.device(device):
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("prepare the operator before the capture: its workspace has "
                                    "to be cleared once")
             self._stream0 = _raw_stream(device.index)
 
-    def _zeros(self, size, dtype) -> torch.Tensor:
-        t = torch.zeros(size, dtype=dtype, device=self.device)
-        self._buffers.append(t)
-        return t
-
-    def _ready(self) -> None:
-        """The buffers are cleared, for any stream."""
+    def _buffers(self, *parts) -> list:
+        """Zeros of each (shape, dtype), None for None, in one allocation that is
+        cleared for any stream when this returns."""
+        sizes = [0 if p is None else math.prod(p[0]) * p[1].itemsize for p in parts]
+        starts = list(itertools.accumulate((-(-n // 256) * 256 for n in sizes), initial=0))
+        self._arena = torch.zeros(max(starts[-1], 1), dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             torch.cuda.current_stream().synchronize()
+        return [None if p is None else self._arena[at:at + n].view(p[1]).view(p[0])
+                for p, at, n in zip(parts, starts, sizes)]
 
     def _count(self, n: int) -> int:
         if n > self.rows:
@@ -111,9 +113,7 @@ class _Op:
         (not in a capture: a graph needs the object alive anyway)."""
         with torch.cuda.device(self.device):
             if not torch.cuda.is_current_stream_capturing():
-                s = torch.cuda.current_stream()
-                for t in self._buffers:
-                    t.record_stream(s)
+                self._arena.record_stream(torch.cuda.current_stream())
 
     def _call(self, fn, what: str, args) -> None:
         """fn(*args, stream) on the current stream of the operator's device."""
@@ -156,14 +156,13 @@ class TokenLogProbs(_Op):
             raise ValueError(f"top must be from 0 to {_native.MAX_TOP}, got {top}")
         super().__init__(rows, device)
         self.vocab, self.top = int(vocab), int(top)
-        self.logp = self._zeros(self.rows, torch.float32)
-        self.entropy = self._zeros(self.rows, torch.float32) if entropy else None
-        self.stats = self._zeros((self.rows, 4), torch.float32)
-        self.top_ids = self._zeros((self.rows, self.top), torch.int64) if top else None
-        self.top_logp = self._zeros((self.rows, self.top), torch.float32) if top else None
         size = int(self._lib.bf16d_logprob_workspace_bytes(self.rows, self.vocab, self.top))
-        self._workspace = self._zeros(size, torch.uint8)
-        self._ready()
+        each, alternatives = (self.rows,), (self.rows, self.top)
+        (self.logp, self.entropy, self.stats, self.top_ids, self.top_logp,
+         self._workspace) = self._buffers(
+            (each, torch.float32), (each, torch.float32) if entropy else None,
+            ((self.rows, 4), torch.float32), (alternatives, torch.int64) if top else None,
+            (alternatives, torch.float32) if top else None, ((size,), torch.uint8))
         self._ran = None    # rows of the last run
         at = lambda t: t.data_ptr() if t is not None else None
         self._job = _native.LogprobJob(logp=at(self.logp), entropy=at(self.entropy),
@@ -254,13 +253,11 @@ class PolicyLoss(_Op):
 
     def __init__(self, rows: int, device=None):
         super().__init__(rows, device)
-        self.grad_logp = self._zeros(self.rows, torch.float32)
-        self.grad_entropy = self._zeros(self.rows, torch.float32)
-        self.result = self._zeros(8, torch.float32)
-        self.loss, self.weight, self.kl, self.clipped, self.entropy = self.result[:5].unbind()
         size = int(self._lib.bf16d_policy_loss_workspace_bytes())
-        self._workspace = self._zeros(size, torch.uint8)
-        self._ready()
+        each = ((self.rows,), torch.float32)
+        self.grad_logp, self.grad_entropy, self.result, self._workspace = self._buffers(
+            each, each, ((8,), torch.float32), ((size,), torch.uint8))
+        self.loss, self.weight, self.kl, self.clipped, self.entropy = self.result[:5].unbind()
         self._job = _native.PolicyJob()
         self._fn = self._lib.bf16d_policy_loss
         self._args = (ctypes.byref(self._job), self.result.data_ptr(),
@@ -320,13 +317,11 @@ class RouterBalance(_Op):
             raise ValueError(f"experts must be from 1 to {_native.MAX_EXPERTS}, got {experts}")
         super().__init__(rows, device)
         self.experts = int(experts)
-        self.counts = self._zeros(self.experts, torch.int64)
-        self.result = self._zeros(4, torch.int64)
+        size = int(self._lib.bf16d_balance_workspace_bytes(self.experts))
+        self.counts, self.result, self._workspace = self._buffers(
+            ((self.experts,), torch.int64), ((4,), torch.int64), ((size,), torch.uint8))
         self.loss, self.balance, self.z = self.result.view(torch.float32)[:3].unbind()
         self.tokens = self.result[2]
-        size = int(self._lib.bf16d_balance_workspace_bytes(self.experts))
-        self._workspace = self._zeros(size, torch.uint8)
-        self._ready()
         self._ran = False
         self._coefs = float(balance_coef), float(z_coef)
         self._job = _native.BalanceJob(balance_coef=balance_coef, z_coef=z_coef,
