@@ -17,7 +17,6 @@ namespace bf16d {
 constexpr uint32_t kTurnVectors = 4;   // of a thread
 constexpr uint32_t kLogprobGroups = 256;
 constexpr uint32_t kLogprobWide = 1024;        // threads
-constexpr uint32_t kLogprobWideGroups = 512;
 constexpr uint32_t vector_elems(uint32_t dtype) { return dtype == BF16D_LOGITS_F32 ? 4 : 8; }
 // The most turns of a row for workgroups of `threads`; aligned: all rows start at
 // 16-byte addresses.

@@ -60,30 +60,29 @@ bool count_rows(uint64_t outer, uint64_t inner, uint64_t &rows) {
            inner < kMaxRows;
 }
 
-// How rows are cut: into `parts` workgroups each, enough for `groups` in all, of
-// part_turns turns.
+// How rows are cut: into `parts` workgroups each, enough for kLogprobGroups in all,
+// of part_turns turns.
 struct Cut {
     uint32_t parts, part_turns;
 };
-Cut cut_rows(uint64_t rows, uint32_t turns, uint32_t groups) {
-    const uint64_t wanted = (groups + rows - 1) / rows;
+Cut cut_rows(uint64_t rows, uint32_t turns) {
+    const uint64_t wanted = (kLogprobGroups + rows - 1) / rows;
     const uint32_t parts = uint32_t(std::min<uint64_t>(wanted, turns));
     const uint32_t each = (turns + parts - 1) / parts;
     return Cut{(turns + each - 1) / each, each};   // whole turns each: fewer parts may do
 }
 
-// counters (rows in parts are fewer than the workgroups), then the parts' words
-constexpr uint32_t kMostGroups = std::max(kLogprobGroups, kLogprobWideGroups);
-constexpr size_t kCounterBytes = 4 * size_t(kMostGroups);
+// counters (rows in parts are fewer than kLogprobGroups), then the parts' words
+constexpr size_t kCounterBytes = 4 * size_t(kLogprobGroups);
 size_t logprob_workspace(uint64_t rows, uint32_t turns, uint32_t top) {
     if (rows == 0 || turns <= 1) return 0;
     // rows * ceil(groups / rows) is below groups + rows, and nothing is cut from
     // `groups` rows on
-    const uint64_t cut = std::min<uint64_t>(rows, kMostGroups - 1);
-    const uint64_t words = std::min<uint64_t>(cut * turns, kMostGroups + cut) * (2 + top);
+    const uint64_t cut = std::min<uint64_t>(rows, kLogprobGroups - 1);
+    const uint64_t words = std::min<uint64_t>(cut * turns, kLogprobGroups + cut) * (2 + top);
     return kCounterBytes + 8 * words;
 }
-static_assert(kLogprobWide >= kThreads, "turns of wide workgroups are fewer");
+static_assert(kLogprobWide >= kThreads, "a wide workgroup's turns are fewer");
 
 bool finite(double x) { return std::isfinite(x); }
 
@@ -136,12 +135,9 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     a.vocab = J.vocab;
     a.token_i32 = J.token_dtype == BF16D_IDS_I32;
     a.top = J.top;
-    // wide: with alternatives, and where that is one turn of a workgroup, and the
-    // workgroups one for each CU
     const uint32_t wide_turns = turns_of(J.vocab, J.logits_dtype, at16, kLogprobWide);
     const bool wide = J.top > 0 || (turns > 1 && wide_turns == 1 && rows <= kLogprobGroups);
-    const Cut cut = wide ? cut_rows(rows, wide_turns, kLogprobWideGroups)
-                         : cut_rows(rows, turns, kLogprobGroups);
+    const Cut cut = cut_rows(rows, wide ? wide_turns : turns);
     a.parts = cut.parts;
     a.part_turns = cut.part_turns;
     const bool keep = J.stats && rows * J.vocab * size <= kLogprobKept;

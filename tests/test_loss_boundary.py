@@ -95,8 +95,8 @@ def test_logprob_refuses_a_short_workspace(native):
     # 4 rows of 5 turns each
     wide = dict(vocab=40000, logits_inner=40000)
     need = native.lib().bf16d_logprob_workspace_bytes(4, 40000, 3)
-    assert need >= 4 * 512 + 4 * 5 * 5 * 8
-    assert _logprob(native, size=4 * 512 + 4 * 5 * 5 * 8 - 8, **wide) == E
+    assert need >= 4 * 256 + 4 * 5 * 5 * 8
+    assert _logprob(native, size=4 * 256 + 4 * 5 * 5 * 8 - 8, **wide) == E
     assert _logprob(native, workspace=None, **wide) == E
     assert _logprob(native, workspace=_at(9) + 8, **wide) == E
     assert _logprob(native, workspace=_at(2), **wide) == E        # over an output
@@ -273,9 +273,9 @@ def test_workspaces_grow_with_the_call(native):
     for turns in (2, 3, 7, 33, 5000):
         vocab = turns * 4096
         for rows in (1, 2, 3, 5, 31, 100, 500, 1000, 1023, 1024, 5000):
-            words = (f(rows, vocab, 3) - 2048) // 8
+            words = (f(rows, vocab, 3) - 1024) // 8
             for fewer in {k for k in (1, 2, rows // 2, rows - 1, rows) if 0 < k <= rows}:
-                parts = min(-(-512 // fewer), turns)
+                parts = min(-(-256 // fewer), turns)
                 if parts > 1:
                     assert words >= fewer * parts * 5, (turns, rows, fewer)
     g = native.lib().bf16d_balance_workspace_bytes
