@@ -176,28 +176,35 @@ class TokenLogProbs(_Op):
         self._grad_args = (ctypes.byref(self._grad_job),)
 
     def _rows_of(self, logits, tokens) -> tuple:
-        """(rows; address and strides of the logits, of the tokens, outer, inner)."""
+        """(rows, shape of the logits, their type and the tokens'; address and strides of
+        the logits, of the tokens, outer, inner).  Each question to a tensor takes 0.1 us."""
         if not (isinstance(logits, torch.Tensor) and logits.get_device() == self._index
-                and logits.dtype in _LOGITS):
+                and (kind := _LOGITS.get(logits.dtype)) is not None):
             _refuse(logits, "logits", _LOGITS, (None, self.vocab), self.device)
         shape, strides = logits.shape, logits.stride()
-        if len(shape) not in (2, 3):
+        if not (isinstance(tokens, torch.Tensor) and tokens.get_device() == self._index
+                and (ids := _IDS.get(tokens.dtype)) is not None):
+            _refuse(tokens, "tokens", _IDS, shape[:-1], self.device)
+        places, steps = tokens.shape, tokens.stride()
+        dims = len(shape)
+        if dims == 2:
+            (inner, vocab), outer = shape, 1
+            l_outer = t_outer = 0
+        elif dims == 3:
+            outer, inner, vocab = shape
+            l_outer, t_outer = strides[0], steps[0] if len(steps) == 2 else 0
+        else:
             raise ValueError(f"logits must be (rows, vocab) or (batch, length, vocab), got "
                              f"{tuple(shape)}")
-        rows = shape[:-1]
-        if shape[-1] != self.vocab or (strides[-1] != 1 and self.vocab > 1 and logits.numel()):
-            _refuse(logits, "logits", _LOGITS, (*rows, self.vocab), self.device)
-        if not (isinstance(tokens, torch.Tensor) and tokens.get_device() == self._index
-                and tokens.dtype in _IDS and tokens.shape == rows):
-            _refuse(tokens, "tokens", _IDS, rows, self.device)
-        if len(shape) == 2:
-            outer, inner = 1, shape[0]
-            t_outer, (t_inner,), l_outer = 0, tokens.stride(), 0
-        else:
-            outer, inner = rows
-            (t_outer, t_inner), l_outer = tokens.stride(), strides[0]
-        return (self._count(outer * inner), logits.data_ptr(), l_outer, strides[-2],
-                tokens.data_ptr(), t_outer, t_inner, outer, inner)
+        n = outer * inner
+        if vocab != self.vocab or (strides[-1] != 1 and vocab > 1 and n):
+            _refuse(logits, "logits", _LOGITS, (*shape[:-1], self.vocab), self.device)
+        if len(places) != dims - 1 or places[-1] != inner or (dims == 3 and places[0] != outer):
+            _refuse(tokens, "tokens", _IDS, shape[:-1], self.device)
+        if n > self.rows:
+            self._count(n)
+        return (n, shape, kind, ids, logits.data_ptr(), l_outer, strides[-2], tokens.data_ptr(),
+                t_outer, steps[-1], outer, inner)
 
     def run(self, logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0) -> None:
         """logits: bf16 or fp32, (rows, vocab) or (batch, length, vocab), a row's
@@ -206,9 +213,8 @@ class TokenLogProbs(_Op):
         by, from 2^-20 to 2^20."""
         if not 2.0 ** -20 <= temperature <= 2.0 ** 20:
             raise ValueError(f"temperature must be from 2^-20 to 2^20, got {temperature}")
-        n, *rows = self._rows_of(logits, tokens)
-        _LOGPROB(self._job, 0, *rows, self.vocab, _LOGITS[logits.dtype], _IDS[tokens.dtype],
-                 self.top, temperature)
+        n, _, kind, ids, *rows = self._rows_of(logits, tokens)
+        _LOGPROB(self._job, 0, *rows, self.vocab, kind, ids, self.top, temperature)
         self._call(self._fn, "bf16d_logprob", self._args)
         self._ran = n
 
@@ -217,25 +223,26 @@ class TokenLogProbs(_Op):
         """The gradient of sum(grad_logp * logp + grad_entropy * entropy) by the logits, into
         `out` (their type and shape; the logits themselves are fine).  logits and
         tokens: those of the last run; grad_logp, grad_entropy: float32, one a row."""
-        n, *rows = self._rows_of(logits, tokens)
+        n, shape, kind, ids, x, x_outer, x_inner, y, y_outer, y_inner, outer, inner = \
+            self._rows_of(logits, tokens)
         if n != self._ran:
             raise ValueError(f"{n} rows, but the last run had {self._ran}: backward needs its "
                              f"softmax sums")
-        kind = logits.dtype
         if not (isinstance(out, torch.Tensor) and out.get_device() == self._index
-                and out.dtype == kind and out.shape == logits.shape
-                and (out.stride(-1) == 1 or self.vocab == 1 or not n)):
-            _refuse(out, "out", (kind,), logits.shape, self.device)
+                and out.dtype == logits.dtype and out.shape == shape):
+            _refuse(out, "out", (logits.dtype,), shape, self.device)
         strides = out.stride()
+        if strides[-1] != 1 and self.vocab > 1 and n:
+            _refuse(out, "out", (logits.dtype,), shape, self.device)
         a = _row(grad_logp, "grad_logp", _F32, n, self.device)
         h = 0
         if grad_entropy is not None:
             if self.entropy is None:
                 raise ValueError("grad_entropy needs an operator prepared with entropy=True")
             h = _row(grad_entropy, "grad_entropy", _F32, n, self.device)
-        _LOGPROB_GRAD(self._grad_job, 0, *rows[:6], out.data_ptr(),
-                      strides[0] if len(strides) == 3 else 0, strides[-2], *rows[6:], self.vocab,
-                      _LOGITS[kind], _IDS[tokens.dtype], 0, self._stats, a, h)
+        _LOGPROB_GRAD(self._grad_job, 0, x, x_outer, x_inner, y, y_outer, y_inner,
+                      out.data_ptr(), strides[0] if len(strides) == 3 else 0, strides[-2], outer,
+                      inner, self.vocab, kind, ids, 0, self._stats, a, h)
         self._call(self._grad_fn, "bf16d_logprob_backward", self._grad_args)
 
 
@@ -336,15 +343,18 @@ class RouterBalance(_Op):
         self._grad_args = (ctypes.byref(self._grad_job),)
 
     def _rows_of(self, logits, mask) -> tuple:
-        """(rows, row stride, address of the mask)"""
+        """(rows, shape of the logits, their type, address, row stride, the mask's address)"""
         if not (isinstance(logits, torch.Tensor) and logits.get_device() == self._index
-                and logits.dtype in _LOGITS and logits.dim() == 2):
+                and (kind := _LOGITS.get(logits.dtype)) is not None
+                and len(shape := logits.shape) == 2):
             _refuse(logits, "logits", _LOGITS, (None, self.experts), self.device)
-        n, experts = logits.shape
+        n, experts = shape
         stride, step = logits.stride()
         if experts != self.experts or (step != 1 and experts > 1 and n):
             _refuse(logits, "logits", _LOGITS, (None, self.experts), self.device)
-        return (self._count(n), stride,
+        if n > self.rows:
+            self._count(n)
+        return (n, shape, kind, logits.data_ptr(), stride,
                 0 if mask is None else _row(mask, "mask", _BYTES, n, self.device))
 
     def run(self, logits: torch.Tensor, chosen: torch.Tensor,
@@ -352,19 +362,20 @@ class RouterBalance(_Op):
         """logits: bf16 or fp32, (tokens, experts).  chosen: int64 or int32, (tokens,
         choices), the ids of each token's experts (a negative one is no choice).
         mask: bool or uint8, which tokens count; None: all."""
-        n, stride, seen = self._rows_of(logits, mask)
+        n, _, kind, x, stride, seen = self._rows_of(logits, mask)
         if not (isinstance(chosen, torch.Tensor) and chosen.get_device() == self._index
-                and chosen.dtype in _IDS and chosen.dim() == 2 and chosen.shape[0] == n):
+                and (ids := _IDS.get(chosen.dtype)) is not None
+                and len(shape := chosen.shape) == 2 and shape[0] == n):
             _refuse(chosen, "chosen", _IDS, (n, None), self.device)
-        choices = chosen.shape[1]
+        choices = shape[1]
         if not 1 <= choices <= self.experts:
             raise ValueError(f"chosen must name from 1 to {self.experts} experts a token, got "
                              f"{choices}")
         chosen_stride, step = chosen.stride()
         if step != 1 and choices > 1 and n:
             _refuse(chosen, "chosen", _IDS, (n, None), self.device)
-        _BALANCE(self._job, 0, logits.data_ptr(), chosen.data_ptr(), seen, n, stride,
-                 chosen_stride, self.experts, choices, _LOGITS[logits.dtype], _IDS[chosen.dtype])
+        _BALANCE(self._job, 0, x, chosen.data_ptr(), seen, n, stride, chosen_stride,
+                 self.experts, choices, kind, ids)
         self._call(self._fn, "bf16d_balance", self._args)
         self._ran = True
 
@@ -374,12 +385,13 @@ class RouterBalance(_Op):
         the logits themselves are fine).  logits, mask: those of the last run."""
         if not self._ran:
             raise ValueError("backward needs the counts of a run")
-        n, stride, seen = self._rows_of(logits, mask)
-        kind = logits.dtype
+        n, shape, kind, x, stride, seen = self._rows_of(logits, mask)
         if not (isinstance(out, torch.Tensor) and out.get_device() == self._index
-                and out.dtype == kind and out.shape == logits.shape
-                and (out.stride(1) == 1 or self.experts == 1 or not n)):
-            _refuse(out, "out", (kind,), logits.shape, self.device)
-        _BALANCE_GRAD(self._grad_job, 0, logits.data_ptr(), out.data_ptr(), seen, n, stride,
-                      out.stride(0), self.experts, _LOGITS[kind], *self._coefs, scale)
+                and out.dtype == logits.dtype and out.shape == shape):
+            _refuse(out, "out", (logits.dtype,), shape, self.device)
+        out_stride, step = out.stride()
+        if step != 1 and self.experts > 1 and n:
+            _refuse(out, "out", (logits.dtype,), shape, self.device)
+        _BALANCE_GRAD(self._grad_job, 0, x, out.data_ptr(), seen, n, stride, out_stride,
+                      self.experts, kind, *self._coefs, scale)
         self._call(self._grad_fn, "bf16d_balance_backward", self._grad_args)
