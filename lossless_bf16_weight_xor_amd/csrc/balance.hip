@@ -27,17 +27,16 @@ template <bool kF32, int kVec>
 struct Pieces {
     static constexpr int kPer = kF32 ? 4 : 8;
     static constexpr uint32_t kSize = kF32 ? 4 : 2;
-    uint32_t lanes, sub, held;   // of a row, this lane among them, rows of a wave
+    uint32_t bits, lanes, sub, held;   // lanes = 2^bits of a row, this one, rows of a wave
     uint32_t experts;
     uint32_t start[kVec];
     bool any[kVec];              // whether the lane holds anything there
     float weight[kVec][kPer];    // 1 or 0
 
-    __device__ __forceinline__ explicit Pieces(uint32_t n) : experts(n) {
-        const uint32_t pieces = (n + kPer - 1) / kPer;
-        lanes = pieces >= 64 ? 64u : pieces > 1 ? 1u << (32 - __clz(pieces - 1)) : 1u;
+    __device__ __forceinline__ Pieces(uint32_t n, uint32_t lane_bits) : bits(lane_bits), experts(n) {
+        lanes = 1u << bits;
         sub = threadIdx.x & (lanes - 1);
-        held = 64 / lanes;
+        held = 64u >> bits;
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
             const uint32_t first = (sub + 64 * v) * kPer;
@@ -143,17 +142,15 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         for (uint32_t i = threadIdx.x; i < words; i += kBalanceThreads) s_words[i] = 0;
         __syncthreads();
     };
-    const Pieces<kF32, kVec> P(a.experts);
+    const Pieces<kF32, kVec> P(a.experts, a.lane_bits);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float p[kVec][kPer] = {};
     double squares = 0.0;
     uint32_t tokens = 0;
     bool bad_id = false, bad_row = false;
     const uint32_t step = gridDim.x * kGroupWaves * P.held;
-    uint32_t row = (blockIdx.x * kGroupWaves + wave) * P.held + lane / P.lanes;
-    const uint32_t turns = row - lane / P.lanes < a.rows
-                               ? (a.rows - (row - lane / P.lanes) + step - 1) / step
-                               : 0;   // the same in the whole wave
+    const uint32_t base = (blockIdx.x * kGroupWaves + first_lane(wave)) * P.held;
+    uint32_t row = base + (lane >> P.bits);
     auto id_at = [&](uint32_t r, uint32_t j) {
         return load_id((const uint8_t *)a.chosen +
                            (r * a.chosen_stride + j) * (a.chosen_i32 ? 4 : 8),
@@ -169,12 +166,12 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         if (id >= (int64_t)a.experts) bad_id = true;
         else if (id >= 0) atomicAdd(&s_words[id], 1ull);
     };
-    if (turns) fetch(row);   // while the sums are cleared
+    if (base < a.rows) fetch(row);   // while the sums are cleared
     clear();
-    for (uint32_t t = 0; t < turns; ++t, row += step) {
+    for (uint32_t at = base; at < a.rows; at += step, row += step) {   // a wave's rows
         Turn<kF32, kVec> now = next;
         const int64_t id = next_id;
-        if (t + 1 < turns) fetch(row + step);
+        if (at + step < a.rows) fetch(row + step);
         now.hide();
         const RowSoftmax<kF32, kVec> r(P, now.w);
         if (r.sum != 0.0f) {   // else nothing, or nothing that counts
@@ -298,15 +295,13 @@ template <bool kF32, int kVec>
 __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs a) {
     constexpr int kPer = kF32 ? 4 : 8;
     __shared__ double s_tmp[kWaves];
-    const Pieces<kF32, kVec> P(a.experts);
+    const Pieces<kF32, kVec> P(a.experts, a.lane_bits);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t step = gridDim.x * kWaves * P.held;
-    uint32_t row = (blockIdx.x * kWaves + wave) * P.held + lane / P.lanes;
-    const uint32_t turns = row - lane / P.lanes < a.rows
-                               ? (a.rows - (row - lane / P.lanes) + step - 1) / step
-                               : 0;
+    const uint32_t base = (blockIdx.x * kWaves + first_lane(wave)) * P.held;
+    uint32_t row = base + (lane >> P.bits);
     Turn<kF32, kVec> next;
-    if (turns) next.load(P, a.logits, a.logits_stride, a.mask, row, a.rows);
+    if (base < a.rows) next.load(P, a.logits, a.logits_stride, a.mask, row, a.rows);
     double choices = 0.0;
     for (uint32_t e = threadIdx.x; e < a.experts; e += kThreads) choices += (double)a.counts[e];
     choices = group_total(choices, s_tmp);
@@ -326,9 +321,9 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
                 P.any[v] && e < a.experts ? (float)(by_share * (double)a.counts[e]) : 0.0f;
             held[v][k] = by[v][k] * P.weight[v][k];
         }
-    for (uint32_t t = 0; t < turns; ++t, row += step) {
+    for (uint32_t at = base; at < a.rows; at += step, row += step) {   // a wave's rows
         Turn<kF32, kVec> now = next;
-        if (t + 1 < turns) next.load(P, a.logits, a.logits_stride, a.mask, row + step, a.rows);
+        if (at + step < a.rows) next.load(P, a.logits, a.logits_stride, a.mask, row + step, a.rows);
         now.hide();
         const RowSoftmax<kF32, kVec> r(P, now.w);
         const float inv = r.sum != 0.0f ? __builtin_amdgcn_rcpf(r.sum) : 0.0f;
@@ -338,35 +333,40 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
 #pragma unroll
             for (int k = 0; k < kPer; ++k) inner = fmaf(r.e[v][k], held[v][k], inner);
         inner = lanes_reduce<Add>(inner, P.lanes) * inv;
-        float same = r.sum != 0.0f ? by_lse * r.lse() - inner : 0.0f;
+        float same = r.sum != 0.0f ? (by_lse * r.lse() - inner) * inv : 0.0f;
         if (now.live) same += spoilt;
         if (!now.there) continue;
         float g[kVec][kPer];
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) g[v][k] = r.e[v][k] * inv * (by[v][k] + same);
+            for (int k = 0; k < kPer; ++k) g[v][k] = r.e[v][k] * fmaf(by[v][k], inv, same);
         store_row(g, P, (uint8_t *)a.out + row * a.out_stride * P.kSize);
     }
 }
 
+// log2 of the lanes of a row
+uint32_t lane_bits_of(uint32_t experts, bool f32) {
+    const uint32_t per = f32 ? 4 : 8;
+    uint32_t bits = 0;
+    while (bits < 6 && (per << bits) < experts) ++bits;
+    return bits;
+}
 // workgroups of `waves` waves for the rows: `most`, or a turn each, or one for up to
 // `alone` turns
-uint32_t grid_of(uint32_t rows, uint32_t experts, bool f32, uint32_t waves, uint32_t most,
+uint32_t grid_of(uint32_t rows, uint32_t lane_bits, uint32_t waves, uint32_t most,
                  uint32_t alone) {
-    const uint32_t per = f32 ? 4 : 8, pieces = (experts + per - 1) / per;
-    uint32_t lanes = 1;
-    while (lanes < 64 && lanes < pieces) lanes *= 2;
-    const uint32_t turn = waves * (64 / lanes);
+    const uint32_t turn = waves * (64u >> lane_bits);
     const uint32_t turns = (rows + turn - 1) / turn;
     return turns <= alone ? 1 : turns < most ? turns : most;
 }
 
 }  // namespace
 
-hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream) {
+hipError_t launch_balance(BalanceArgs a, bool f32, hipStream_t stream) {
+    a.lane_bits = lane_bits_of(a.experts, f32);
     const uint32_t grid =
-        grid_of(a.rows, a.experts, f32, kBalanceThreads / 64, kBalanceGrid, kBalanceAlone);
+        grid_of(a.rows, a.lane_bits, kBalanceThreads / 64, kBalanceGrid, kBalanceAlone);
     auto *kernel = f32 ? (a.experts <= 256   ? balance_kernel<true, 1>
                           : a.experts <= 512 ? balance_kernel<true, 2>
                                              : balance_kernel<true, 4>)
@@ -374,8 +374,9 @@ hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream) {
     return launch_one(kernel, grid, kBalanceThreads, a, 0, stream);
 }
 
-hipError_t launch_balance_backward(const BalanceGradArgs &a, bool f32, hipStream_t stream) {
-    const uint32_t grid = grid_of(a.rows, a.experts, f32, kWaves, kBalanceGradGrid, 1);
+hipError_t launch_balance_backward(BalanceGradArgs a, bool f32, hipStream_t stream) {
+    a.lane_bits = lane_bits_of(a.experts, f32);
+    const uint32_t grid = grid_of(a.rows, a.lane_bits, kWaves, kBalanceGradGrid, 1);
     auto *kernel =
         f32 ? (a.experts <= 256   ? balance_grad_kernel<true, 1>
                : a.experts <= 512 ? balance_grad_kernel<true, 2>

@@ -91,7 +91,7 @@ struct BalanceArgs {
     const void *logits, *chosen;
     const uint8_t *mask;
     uint64_t logits_stride, chosen_stride;
-    uint32_t rows, experts, choices, chosen_i32;
+    uint32_t rows, experts, choices, chosen_i32, lane_bits;
     double balance_coef, z_coef;
     int64_t *counts;
     bf16d_balance_result *result;
@@ -99,19 +99,19 @@ struct BalanceArgs {
     uint64_t *partial;   // a workgroup's sum of squares
     uint32_t *done;      // kDoneWords
 };
-hipError_t launch_balance(const BalanceArgs &a, bool f32, hipStream_t stream);
+hipError_t launch_balance(BalanceArgs a, bool f32, hipStream_t stream);
 
 struct BalanceGradArgs {
     const void *logits;
     void *out;
     const uint8_t *mask;
     uint64_t logits_stride, out_stride;
-    uint32_t rows, experts;
+    uint32_t rows, experts, lane_bits;
     double balance_coef, z_coef, scale;
     const int64_t *counts, *tokens;
     const bf16d_balance_result *result;
 };
-hipError_t launch_balance_backward(const BalanceGradArgs &a, bool f32, hipStream_t stream);
+hipError_t launch_balance_backward(BalanceGradArgs a, bool f32, hipStream_t stream);
 
 // ---- device helpers -----------------------------------------------------------------
 typedef uint32_t word4 __attribute__((ext_vector_type(4)));
