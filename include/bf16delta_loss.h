@@ -74,7 +74,7 @@ typedef struct bf16d_row_stats {
  * A logit of -infinity is a token that cannot occur: its p is 0, it adds nothing
  * to H, and it is no alternative (as a given token it has logp = -infinity).
  * Where fewer than `top` are left, the rest has id -1 and logp -infinity.
- *   - a negative token leaves its row out: its logits are not read, logp and
+ *   - a negative token leaves its row out: whatever its logits are, logp and
  *     entropy are 0, and it has no alternatives;
  *   - a row of nothing but -infinity has logp = -infinity, entropy 0 and no
  *     alternatives;
@@ -84,9 +84,9 @@ typedef struct bf16d_row_stats {
  * Logits of any finite size are fine, a mask of the type's lowest value among
  * them.
  *
- * temperature: from 2^-20 to 2^20.  outer * inner is below 2^24, vocab from 1
- * to BF16D_MAX_VOCAB, top at most BF16D_MAX_TOP.  With no rows, pointers may be
- * NULL. */
+ * temperature: from 2^-20 to 2^20.  outer * inner is below 2^24 (with alternatives
+ * below 2^22), vocab from 1 to BF16D_MAX_VOCAB, top at most BF16D_MAX_TOP.  With no
+ * rows, pointers may be NULL. */
 typedef struct bf16d_logprob_job {
     bf16d_rows       logits;        /* of logits_dtype, BF16D_LOGITS_* */
     bf16d_rows       tokens;        /* of token_dtype, BF16D_IDS_*; one id a row */

@@ -10,7 +10,8 @@ using namespace bf16d;
 
 namespace {
 
-constexpr uint64_t kMaxRows = 1ull << 24;      // below this
+constexpr uint64_t kMaxRows = 1ull << 24;      // below this: a workgroup each, 2^32 threads
+constexpr uint64_t kMaxWideRows = kMaxRows * kThreads / kLogprobWide;
 constexpr uint64_t kMaxTokens = 1ull << 40;
 
 bool aligned(const void *p, uint64_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -93,7 +94,8 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     uint64_t rows = 0;
     if (!count_rows(J.outer, J.inner, rows) || J.vocab == 0 || J.vocab > BF16D_MAX_VOCAB ||
         J.logits_dtype > BF16D_LOGITS_F32 || J.token_dtype > BF16D_IDS_I32 ||
-        J.top > BF16D_MAX_TOP || !(J.temperature >= 0x1p-20) || !(J.temperature <= 0x1p20))
+        J.top > BF16D_MAX_TOP || (J.top > 0 && rows >= kMaxWideRows) ||
+        !(J.temperature >= 0x1p-20) || !(J.temperature <= 0x1p20))
         return BF16D_EINVAL;
     if (!aligned16(J.logp) || !aligned16(J.entropy) || !aligned16(J.stats) ||
         !aligned16(J.top_ids) || !aligned16(J.top_logp) || !aligned16(workspace) ||

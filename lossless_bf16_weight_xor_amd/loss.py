@@ -154,6 +154,8 @@ class TokenLogProbs(_Op):
             raise ValueError(f"vocab must be from 1 to {_native.MAX_VOCAB}, got {vocab}")
         if not 0 <= top <= _native.MAX_TOP:
             raise ValueError(f"top must be from 0 to {_native.MAX_TOP}, got {top}")
+        if top and not rows < 1 << 22:
+            raise ValueError(f"rows must be below 2^22 with alternatives, got {rows}")
         super().__init__(rows, device)
         self.vocab, self.top = int(vocab), int(top)
         size = int(self._lib.bf16d_logprob_workspace_bytes(self.rows, self.vocab, self.top))

@@ -149,6 +149,27 @@ def test_balance_of_one_expert_and_of_none(rows):
         assert (op.counts == 0).all() and op.balance == 0 and op.tokens == rows
 
 
+def test_operators_for_no_rows():
+    log("prepared for no rows")
+    empty = torch.empty(0, device=DEV)
+    for top, entropy in ((0, False), (3, True)):
+        op = TokenLogProbs(0, 50, DEV, entropy=entropy, top=top)
+        x, y = torch.empty(0, 50, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV)
+        op.run(x, y)
+        op.backward(x, y, empty, x)
+        with pytest.raises(ValueError, match="prepared for 0"):
+            op.run(torch.empty(1, 50, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV))
+    loss = PolicyLoss(0, DEV)
+    loss.result.fill_(7.0)
+    loss.run(empty, empty, empty, entropy=empty)
+    assert (loss.result[:5] == 0).all()
+    router = RouterBalance(0, 50, DEV)
+    router.counts.fill_(7)
+    router.run(x, torch.empty(0, 2, dtype=torch.int32, device=DEV))
+    router.backward(x, x)
+    assert router.tokens == 0 and router.loss == 0 and (router.counts == 0).all()
+
+
 def test_buffers_are_held_for_another_stream(monkeypatch):
     """A run on another stream than the buffers' own tells torch's allocator."""
     log("held")

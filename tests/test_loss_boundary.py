@@ -84,6 +84,7 @@ def test_logprob_refusals(native):
     for outer, inner in ((1, 1 << 24), (1 << 24, 1), (1 << 13, 1 << 13), (1 << 40, 1 << 40),
                          (0, 1 << 24)):
         assert call(outer=outer, inner=inner) == E
+    assert call(inner=1 << 22) == E          # alternatives of as many rows
     for name in ("logits_inner", "tokens_inner"):
         for stride in (1 << 61, (1 << 64) - 1):
             assert call(**{name: stride}) == E
@@ -297,6 +298,8 @@ def test_python_api_refuses_cpu_tensors_and_bad_sizes(native):
     for experts in (0, 1025):
         with pytest.raises(ValueError, match="experts"):
             RouterBalance(4, experts)
+    with pytest.raises(ValueError, match="below 2\\^22"):
+        TokenLogProbs(1 << 22, 100, top=1)
     for rows in (-1, 1 << 24):
         for make in (lambda: TokenLogProbs(rows, 100, "cuda:0"), lambda: PolicyLoss(rows, "cuda:0"),
                      lambda: RouterBalance(rows, 8, "cuda:0")):
