@@ -8,6 +8,11 @@
 // So softmax sums are a few lane steps, and a lane's sums of p over its rows stay
 // in registers.  Lanes and workgroups add up in integers (counts, and sums of p
 // in steps of 2^-36), so the order of their atomics does not matter.
+//
+// 65536 rows of 64 fp32 experts: 12.8 us forward, of which launch and join are 8, and
+// 9.4 backward (3.6 TB/s); 32768 rows of 257 bf16 experts 21 and 17, bound by the
+// vector units (93 % of the issue slots backward): a row is 33 pieces, so half of
+// each wave idles.
 #include "loss.hpp"
 
 namespace bf16d {

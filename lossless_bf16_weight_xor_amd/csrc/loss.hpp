@@ -11,11 +11,17 @@
 namespace bf16d {
 
 // ---- log probabilities --------------------------------------------------------
-// A row is read in turns: four 16-byte vectors a thread.  Rows are cut into
-// parts of whole turns, one workgroup each, where there are fewer rows than
-// kLogprobGroups.
+// A row is read in turns, four 16-byte vectors a thread, by one workgroup where
+// there are at least kLogprobGroups rows (one for each CU), else cut into parts of
+// whole turns so that there are as many workgroups.  More of them gain less than
+// the joining costs: 256 rows of 131072 bf16 logits 13.4 us, cut for 512 and
+// 1024 workgroups 15.1 and 16.1; one row 4.6, 4.6 and 4.5.
 constexpr uint32_t kTurnVectors = 4;   // of a thread
 constexpr uint32_t kLogprobGroups = 256;
+// Workgroups of 16 waves hold a row of up to 32768 bf16 or 16384 fp32 logits in one
+// turn and need no join: 96 rows of 32000 bf16 5.2 us, in parts 6.2; 8000 fp32 4.3
+// and 5.1.  A row of more than that is faster in parts (one of 50021 bf16 5.5 and
+// 6.3), except with alternatives, which are found by such workgroups.
 constexpr uint32_t kLogprobWide = 1024;        // threads
 constexpr uint32_t vector_elems(uint32_t dtype) { return dtype == BF16D_LOGITS_F32 ? 4 : 8; }
 // The most turns of a row for workgroups of `threads`; aligned: all rows start at
@@ -25,7 +31,10 @@ inline uint32_t turns_of(uint32_t vocab, uint32_t dtype, bool aligned, uint32_t 
     return (vocab + (aligned ? 0 : vector_elems(dtype) - 1) + per - 1) / per;
 }
 // Logits of up to this many bytes are left in the last-level cache for the
-// backward pass.
+// backward pass; more are read with non-temporal loads (fp32, 16384 x 32000: 307
+// us, plain 343).  Forward and backward of bf16 logits with and without: 66 MB 38.9
+// and 42.1 us, 131 MB 72.5 and 75.1; of 262 MB in fp32 131.6 and 127.3, and the
+// forward pass alone 47.8 and 42.2.
 constexpr uint64_t kLogprobKept = 128u << 20;
 
 // Rows of a call, as the device sees them.
@@ -62,6 +71,7 @@ struct LogprobGradArgs {
 hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream_t stream);
 
 // ---- policy loss ----------------------------------------------------------------
+// A workgroup of 16 waves for each CU at most: 1e6 tokens 9.6 us, with 4 waves 28.
 constexpr uint32_t kPolicyGrid = 256;
 constexpr uint32_t kPolicyThreads = 1024;
 constexpr uint32_t kPolicyAlone = 2;   // turns that one workgroup takes sooner than joining sums
@@ -80,13 +90,18 @@ struct PolicyArgs {
 hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream);
 
 // ---- balance loss ------------------------------------------------------------------
-// A workgroup of 16 waves for each CU: as many rows in flight as with small
-// ones, and fewer additions to the shared sums at the end.
+// A workgroup of 16 waves for each CU: as many rows in flight as with small ones,
+// and fewer that add to the shared sums at the end (with 512 workgroups 65536 rows of
+// 64 fp32 experts took 19.1 us instead of 14.4).
 constexpr uint32_t kBalanceGrid = 256;
 constexpr uint32_t kBalanceThreads = 1024;
 constexpr uint32_t kBalanceAlone = 4;        // turns that one takes sooner than joining sums
-constexpr uint32_t kBalanceCopies = 8;       // of the sums that workgroups add to
-constexpr uint32_t kBalanceGradGrid = 2048;   // of four waves
+// of the sums that workgroups add to: 16384 rows of 64 fp32 experts 11.4 us, with one
+// copy 14.4
+constexpr uint32_t kBalanceCopies = 8;
+// of four waves: as many as are resident at once (65536 rows of 256 bf16 experts 18.0 us,
+// with 1024 19.0, with 4096 20.9)
+constexpr uint32_t kBalanceGradGrid = 2048;
 struct BalanceArgs {
     const void *logits, *chosen;
     const uint8_t *mask;
@@ -147,7 +162,8 @@ __device__ __forceinline__ bool last_of(uint32_t *done, uint32_t count, uint64_t
 }
 
 // The same for all workgroups of a launch, in two levels: additions to one address
-// take 20 ns each, 5 us for 256 workgroups.  done: kDoneWords counters.
+// take some 10 to 20 ns each (1e6 tokens of the policy loss, 256 workgroups: 9.6 us, in
+// one level 11.3).  done: kDoneWords counters.
 constexpr uint32_t kDoneGroups = 16, kDoneStride = 32;   // words: a line each
 constexpr uint32_t kDoneWords = (kDoneGroups + 1) * kDoneStride;
 __device__ __forceinline__ bool last_of_launch(uint32_t *done, uint64_t dep) {

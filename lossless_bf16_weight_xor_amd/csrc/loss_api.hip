@@ -137,6 +137,7 @@ int logprob(const bf16d_logprob_job *job, void *workspace, size_t workspace_byte
     a.vocab = J.vocab;
     a.token_i32 = J.token_dtype == BF16D_IDS_I32;
     a.top = J.top;
+    // see kLogprobWide
     const uint32_t wide_turns = turns_of(J.vocab, J.logits_dtype, at16, kLogprobWide);
     const bool wide = J.top > 0 || (turns > 1 && wide_turns == 1 && rows <= kLogprobGroups);
     const Cut cut = cut_rows(rows, wide ? wide_turns : turns);
