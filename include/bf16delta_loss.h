@@ -82,7 +82,9 @@ typedef struct bf16d_row_stats {
  *     top_logp NaN (NaN is no alternative);
  *   - a token from `vocab` on has logp = NaN.
  * Logits of any finite size are fine, a mask of the type's lowest value among
- * them.
+ * them.  A log probability below fp32's range (the lowest value over a temperature
+ * below 1) is -infinity; as an alternative it keeps its id, and its p of 0 adds
+ * nothing to H or to a gradient.
  *
  * temperature: from 2^-20 to 2^20.  outer * inner is below 2^24 (with alternatives
  * below 2^22), vocab from 1 to BF16D_MAX_VOCAB, top at most BF16D_MAX_TOP.  With no

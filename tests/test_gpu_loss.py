@@ -189,6 +189,41 @@ def test_rows_that_are_special(kind, vocab):
     ref.check(got[fine[:-1]], grad[:-1], off[:-1], "grad in place")
 
 
+@both_types
+@pytest.mark.parametrize("vocab", [50, 40000])
+def test_log_probabilities_below_the_range_of_fp32(kind, vocab):
+    """The lowest value over a small temperature: -infinity as a number, finite in a gradient."""
+    log(f"{kind} {vocab}")
+    low = torch.finfo(TYPES[kind]).min
+    x = _logits(4, vocab, 31, kind)
+    y = _tokens(4, vocab, 31)
+    x[0, 1:] = low             # one of weight, the given token another
+    y[0] = 3
+    x[1] = low                 # even: nothing is below the range
+    x[2, ::2] = low
+    x[2, y[2]] = 1.0
+    x[3, y[3]] = low
+    top = 5
+    op = TokenLogProbs(4, vocab, DEV, entropy=True, top=top)
+    dx, dy = x.to(DEV), y.to(DEV)
+    op.run(dx, dy, temperature=0.05)
+    want = ref.Rows(x, y, 0.05, top=top)
+    # what lies below -max rounds to -infinity in fp32
+    below = lambda t: t < -torch.finfo(torch.float32).max
+    for got, value, off in ((op.logp.cpu(), want.logp, want.logp_off),
+                            (op.top_logp.cpu(), want.top_logp, want.top_off)):
+        assert (got[below(value)] == -INF).all()
+        ref.check(got[~below(value)], value[~below(value)], off[~below(value)], "logp")
+    assert below(want.logp).tolist() == [True, False, False, True]
+    assert torch.equal(op.top_ids.cpu(), want.top_ids)
+    ref.check(op.entropy.cpu(), want.entropy[:, 0], want.h_off[:, 0], "entropy")
+    a, g = _coefs(4, 9)
+    out = torch.full_like(dx, 7.0)
+    op.backward(dx, dy, a.to(DEV), out, grad_entropy=g.to(DEV))
+    grad, off = want.grad(a, g, x.dtype)
+    ref.check(out.cpu(), grad, off, "grad")
+
+
 def _strided(kind, vocab, seed):
     """Views of wider buffers: (name, logits, tokens, out) factories over (3, 5) rows."""
     dt = TYPES[kind]
