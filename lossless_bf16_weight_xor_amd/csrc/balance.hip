@@ -3,16 +3,15 @@
 //
 // The gradient of balance = E sum f_e P_e needs every f_e, so it is a pass of
 // its own: the first one sums p and counts, the second one computes p again.
-// A lane holds 16 bytes of neighbouring experts (a row of more than 64 such
-// pieces: two or four), a row the next power of two of lanes, a wave 64 / lanes rows.
-// So softmax sums are a few lane steps, and a lane's sums of p over its rows stay
-// in registers.  Lanes and workgroups add up in integers (counts, and sums of p
+// A row is cut into pieces of 16 bytes of neighbouring experts.  A lane holds one to
+// four of them, a row a power of two of lanes, a wave 64 / lanes rows.  So softmax sums
+// are a few lane steps for several rows at once, and a lane's sums of p over its rows
+// stay in registers.  Lanes and workgroups add up in integers (counts, and sums of p
 // in steps of 2^-36), so the order of their atomics does not matter.
 //
-// 65536 rows of 64 fp32 experts: 12.8 us forward, of which launch and join are 8, and
-// 9.4 backward (3.6 TB/s); 32768 rows of 257 bf16 experts 21 and 17, bound by the
-// vector units (93 % of the issue slots backward): a row is 33 pieces, so half of
-// each wave idles.
+// 65536 rows of 64 fp32 experts: 11.7 us forward, of which launch and join are 8, and
+// 8.6 backward (3.9 TB/s); 32768 rows of 257 bf16 experts 16.2 and 11.5 (1024 of them:
+// 10.4 and 3.8), 131072 of them 29.5 and 29 (2.5 and 4.7 TB/s).
 #include "loss.hpp"
 
 namespace bf16d {
@@ -25,9 +24,10 @@ constexpr double kFixed = 68719476736.0;   // 2^36: sums of p stay below 2^24 ro
 enum { kSumTokens = 0, kSumBadIds = 1, kSumBadRows = 2, kSumWords = 3 };
 
 // Which experts a lane holds: kVec pieces of kPer neighbours, piece v from
-// start[v] on.  The last piece of a row ends where the row ends, so that all pieces
-// are whole loads; what it shares with the one before has weight 0 in sums,
-// and both lanes store the same values there.
+// start[v] on, 2^bits pieces apart.  The last piece of a row ends where the row ends, so
+// that all pieces are whole loads; what it shares with the one before has weight 0
+// in sums, and both lanes store the same values there.  A row has more than kVec - 1
+// pieces for each lane, so only a lane's last one can be that piece, or none.
 template <bool kF32, int kVec>
 struct Pieces {
     static constexpr int kPer = kF32 ? 4 : 8;
@@ -35,23 +35,40 @@ struct Pieces {
     uint32_t bits, lanes, sub, held;   // lanes = 2^bits of a row, this one, rows of a wave
     uint32_t experts;
     uint32_t start[kVec];
-    bool any[kVec];              // whether the lane holds anything there
-    float weight[kVec][kPer];    // 1 or 0
+    bool any;              // whether the lane holds a last one
+    float weight[kPer];    // of that: 1 or 0
 
     __device__ __forceinline__ Pieces(uint32_t n, uint32_t lane_bits) : bits(lane_bits), experts(n) {
         lanes = 1u << bits;
         sub = threadIdx.x & (lanes - 1);
         held = 64u >> bits;
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const uint32_t first = (sub + 64 * v) * kPer;
-            const uint32_t last = n < kPer ? 0 : n - kPer;
-            start[v] = first < last ? first : last;
-            any[v] = first < n;
+        for (int v = 0; v < kVec - 1; ++v) start[v] = (sub + lanes * v) * kPer;
+        const uint32_t first = (sub + lanes * (kVec - 1)) * kPer;
+        const uint32_t last = n < kPer ? 0 : n - kPer;
+        start[kVec - 1] = first < last ? first : last;
+        any = first < n;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                weight[v][k] = start[v] + k >= first && start[v] + k < n ? 1.0f : 0.0f;
+        for (int k = 0; k < kPer; ++k)
+            weight[k] =
+                start[kVec - 1] + k >= first && start[kVec - 1] + k < n ? 1.0f : 0.0f;
+    }
+    __device__ __forceinline__ bool holds(int v) const { return v < kVec - 1 || any; }
+    // x[v][k] times a factor of its own, summed over the lane's experts in short chains
+    template <typename F>
+    __device__ __forceinline__ float total(const float (&x)[kVec][kPer], F factor) const {
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            float a = x[v][0] * factor(v, 0), b = x[v][1] * factor(v, 1);
+#pragma unroll
+            for (int k = 2; k < kPer; k += 2) {
+                a = fmaf(x[v][k], factor(v, k), a);
+                b = fmaf(x[v][k + 1], factor(v, k + 1), b);
+            }
+            sum = v ? sum + (a + b) : a + b;
         }
+        return sum;
     }
 };
 
@@ -81,7 +98,7 @@ struct Turn {
         for (int v = 0; v < kVec; ++v) {
             const uint8_t *p = at + P.start[v] * P.kSize;
             if (P.experts >= kPer) {
-                if (P.any[v]) w[v] = *(const word4_any *)p;
+                if (P.holds(v)) w[v] = *(const word4_any *)p;
                 continue;
             }
 #pragma unroll
@@ -119,15 +136,13 @@ struct RowSoftmax {
             for (int k = 0; k < kPer; ++k) m = fmaxf(m, element<kF32>(w[v], k));
         m = lanes_reduce<Max>(m, P.lanes);
         if (m == -INFINITY) m = 0.0f;
-        float s = 0.0f;
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
+            for (int k = 0; k < kPer; ++k)
                 e[v][k] = __builtin_amdgcn_exp2f((element<kF32>(w[v], k) - m) * kLog2E);
-                s = fmaf(e[v][k], P.weight[v][k], s);
-            }
-        sum = lanes_reduce<Add>(s, P.lanes);
+        sum = lanes_reduce<Add>(
+            P.total(e, [&](int v, int k) { return v < kVec - 1 ? 1.0f : P.weight[k]; }), P.lanes);
     }
     // the hardware's log2, good to one unit in the last place
     __device__ __forceinline__ float lse() const { return m + kLn2 * __builtin_amdgcn_logf(sum); }
@@ -137,7 +152,8 @@ template <bool kF32, int kVec>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a) {
     constexpr int kPer = kF32 ? 4 : 8;
     constexpr uint32_t kGroupWaves = kBalanceThreads / 64;
-    constexpr uint32_t kMost = 64 * kVec * kPer;
+    constexpr uint32_t kMost = BF16D_MAX_EXPERTS;
+    constexpr uint32_t kWordsEach = (2 * kMost + kSumWords + kBalanceThreads - 1) / kBalanceThreads;
     // counts, sums of p, and what else is summed
     __shared__ unsigned long long s_words[2 * kMost + kSumWords];
     __shared__ double s_sum[kGroupWaves][3];
@@ -197,13 +213,35 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     if (tokens) atomicAdd(&s_more[kSumTokens], (unsigned long long)tokens);
     if (bad_id) s_more[kSumBadIds] = 1;
     if (bad_row) s_more[kSumBadRows] = 1;
+    // Rows of up to 16 lanes: the sums of a wave's four quarters are added up first, and
+    // each quarter hands over a fourth of them.
+    const uint32_t quarter = lane >> 4;
+    auto add_p = [&](int v, uint32_t k, float x, float weight) {
+        if (weight != 0.0f && x > 0.0f && x < INFINITY)
+            atomicAdd(&s_words[a.experts + P.start[v] + k],
+                      (unsigned long long)__double2ll_rn((double)x * kFixed));
+    };
+    auto weight = [&](int v, int k) { return v < kVec - 1 ? 1.0f : P.weight[k]; };
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (P.weight[v][k] != 0.0f && p[v][k] > 0.0f && p[v][k] < INFINITY)
-                atomicAdd(&s_words[a.experts + P.start[v] + k],
-                          (unsigned long long)__double2ll_rn((double)p[v][k] * kFixed));
+        for (int k = 0; k < kPer; k += 4) {
+            if (P.bits > 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) add_p(v, k + j, p[v][k + j], weight(v, k + j));
+                continue;
+            }
+            float x = 0.0f, of = 0.0f;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                float even, odd;
+                both_halves<32>(p[v][k + j], even, odd);
+                both_halves<16>(even + odd, even, odd);
+                x = quarter == j ? even + odd : x;
+                of = quarter == j ? weight(v, k + j) : of;
+            }
+            add_p(v, k + quarter, x, of);
+        }
     // sums over the workgroup, a value a lane, in a fixed order
     auto totals = [&](double (&x)[3]) {
 #pragma unroll
@@ -224,23 +262,38 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         // Every workgroup adds to one of kBalanceCopies copies of the sums: additions
         // to one address by all 256 take 4 us.
         uint64_t *copy = a.sums + (uint64_t)(blockIdx.x % kBalanceCopies) * words;
-        uint64_t dep = 0;
-        for (uint32_t i = threadIdx.x; i < words; i += kBalanceThreads)
-            if (s_words[i])
-                dep ^= __hip_atomic_fetch_add(copy + i, (uint64_t)s_words[i], __ATOMIC_RELAXED,
-                                              __HIP_MEMORY_SCOPE_AGENT);
+        uint64_t dep = 0, was[kWordsEach] = {};
+#pragma unroll
+        for (uint32_t k = 0; k < kWordsEach; ++k) {
+            const uint32_t i = threadIdx.x + k * kBalanceThreads;
+            if (i < words && s_words[i])
+                was[k] = __hip_atomic_fetch_add(copy + i, (uint64_t)s_words[i], __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kWordsEach; ++k) dep ^= was[k];
         if (threadIdx.x == kBalanceThreads - 1)
             dep ^= __hip_atomic_exchange(a.partial + blockIdx.x,
                                          (uint64_t)__double_as_longlong(x[0]), __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT);
         if (!last_of_launch(a.done, dep)) return;
         clear();
-        // the copies are read and cleared
+        // The copies are read and cleared, kAhead words of a thread at once: 1024 rows of 1024
+        // bf16 experts 15.6 us, one word at a time 19.2 (257 experts 10.4 and 11.0).
         const uint32_t copies = gridDim.x < kBalanceCopies ? gridDim.x : kBalanceCopies;
-        for (uint32_t i = threadIdx.x; i < copies * words; i += kBalanceThreads) {
-            const uint64_t v = __hip_atomic_exchange(a.sums + i, (uint64_t)0, __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-            if (v) atomicAdd(&s_words[i % words], (unsigned long long)v);
+        constexpr uint32_t kAhead = 6;
+        for (uint32_t i = threadIdx.x; i < copies * words; i += kAhead * kBalanceThreads) {
+            uint64_t v[kAhead] = {};
+#pragma unroll
+            for (uint32_t k = 0; k < kAhead; ++k)
+                if (i + k * kBalanceThreads < copies * words)
+                    v[k] = __hip_atomic_exchange(a.sums + i + k * kBalanceThreads, (uint64_t)0,
+                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (uint32_t k = 0; k < kAhead; ++k)
+                if (v[k])
+                    atomicAdd(&s_words[(i + k * kBalanceThreads) % words],
+                              (unsigned long long)v[k]);
         }
         static_assert(kBalanceGrid <= kBalanceThreads, "a thread takes one workgroup's sum");
         x[0] = threadIdx.x < gridDim.x
@@ -284,7 +337,7 @@ __device__ __forceinline__ void store_row(const float (&g)[kVec][kPer],
             else w[k] = pack_bf16(g[v][2 * k], g[v][2 * k + 1]);
         }
         if (P.experts >= kPer) {
-            if (P.any[v]) *(word4_any *)p = w;
+            if (P.holds(v)) *(word4_any *)p = w;
             continue;
         }
 #pragma unroll
@@ -300,6 +353,7 @@ template <bool kF32, int kVec>
 __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs a) {
     constexpr int kPer = kF32 ? 4 : 8;
     __shared__ double s_tmp[kWaves];
+    __shared__ float s_by[BF16D_MAX_EXPERTS];
     const Pieces<kF32, kVec> P(a.experts, a.lane_bits);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t step = gridDim.x * kWaves * P.held;
@@ -307,8 +361,14 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
     uint32_t row = base + (lane >> P.bits);
     Turn<kF32, kVec> next;
     if (base < a.rows) next.load(P, a.logits, a.logits_stride, a.mask, row, a.rows);
-    double choices = 0.0;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kThreads) choices += (double)a.counts[e];
+    constexpr uint32_t kShare = BF16D_MAX_EXPERTS / kThreads;
+    double chosen[kShare], choices = 0.0;
+#pragma unroll
+    for (uint32_t i = 0; i < kShare; ++i) {
+        const uint32_t e = i * kThreads + threadIdx.x;
+        chosen[i] = e < a.experts ? (double)a.counts[e] : 0.0;
+        choices += chosen[i];
+    }
     choices = group_total(choices, s_tmp);
     const double n = *a.tokens > 1 ? (double)*a.tokens : 1.0;
     // of one choice
@@ -316,15 +376,18 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
         choices > 0.0 ? a.scale * a.balance_coef * a.experts / n / choices : 0.0;
     const float by_lse = (float)(2.0 * a.scale * a.z_coef / n);
     const float spoilt = a.result && a.result->loss != a.result->loss ? NAN : 0.0f;
-    float by[kVec][kPer], held[kVec][kPer];   // an expert's factor, and the same weighted
+#pragma unroll
+    for (uint32_t i = 0; i < kShare; ++i)
+        s_by[i * kThreads + threadIdx.x] = (float)(by_share * chosen[i]);
+    __syncthreads();
+    float by[kVec][kPer], held[kPer];   // an expert's factor; of the last piece, weighted
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const uint32_t e = P.start[v] + k;
-            by[v][k] =
-                P.any[v] && e < a.experts ? (float)(by_share * (double)a.counts[e]) : 0.0f;
-            held[v][k] = by[v][k] * P.weight[v][k];
+            by[v][k] = P.holds(v) && e < a.experts ? s_by[e] : 0.0f;
+            if (v == kVec - 1) held[k] = by[v][k] * P.weight[k];
         }
     for (uint32_t at = base; at < a.rows; at += step, row += step) {   // a wave's rows
         Turn<kF32, kVec> now = next;
@@ -332,12 +395,8 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
         now.hide();
         const RowSoftmax<kF32, kVec> r(P, now.w);
         const float inv = r.sum != 0.0f ? __builtin_amdgcn_rcpf(r.sum) : 0.0f;
-        float inner = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kVec; ++v)
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) inner = fmaf(r.e[v][k], held[v][k], inner);
-        inner = lanes_reduce<Add>(inner, P.lanes) * inv;
+        const float inner = inv * lanes_reduce<Add>(
+            P.total(r.e, [&](int v, int k) { return v < kVec - 1 ? by[v][k] : held[k]; }), P.lanes);
         float same = r.sum != 0.0f ? (by_lse * r.lse() - inner) * inv : 0.0f;
         if (now.live) same += spoilt;
         if (!now.there) continue;
@@ -350,12 +409,31 @@ __global__ __launch_bounds__(kThreads) void balance_grad_kernel(BalanceGradArgs 
     }
 }
 
-// log2 of the lanes of a row
-uint32_t lane_bits_of(uint32_t experts, bool f32) {
+// How a row is held: by 2^bits lanes of `vec` pieces each.
+struct Hold {
+    uint32_t bits, vec;
+};
+uint32_t pieces_of(uint32_t experts, bool f32) {
     const uint32_t per = f32 ? 4 : 8;
+    return (experts + per - 1) / per;
+}
+// Few lanes take fewer steps to join, for more rows at once, and leave fewer lanes idle:
+// 131072 rows of 257 bf16 experts 30 us forward and 29 backward, with a piece a lane 53 and 48;
+// of 64 fp32 experts 15.7 and 13.6, 17.2 and 13.3.  Fewer than 8 lanes load too
+// scattered (65536 rows of 64, 4 lanes: 17 and 17), and four pieces of 8 do not fit into the
+// registers of a workgroup of 16 waves.
+Hold fewest_lanes(uint32_t pieces, bool f32) {
     uint32_t bits = 0;
-    while (bits < 6 && (per << bits) < experts) ++bits;
-    return bits;
+    auto most = [&] { return bits < 3 ? 1u : bits == 3 ? 2u : f32 ? 4u : 3u; };
+    while (bits < 6 && pieces > most() << bits) ++bits;
+    return Hold{bits, (pieces + (1u << bits) - 1) >> bits};
+}
+// The same with more lanes, as long as there are so many in all: 4096 rows of 257 bf16
+// experts 12.2 us forward and 5.1 backward, with the fewest 13.9 and 6.5.
+Hold more_lanes(Hold h, uint32_t pieces, uint32_t rows, uint32_t threads) {
+    while (h.bits < 6 && pieces > 1u << h.bits && (uint64_t)rows << (h.bits + 1) <= threads)
+        ++h.bits;
+    return Hold{h.bits, (pieces + (1u << h.bits) - 1) >> h.bits};
 }
 // workgroups of `waves` waves for the rows: `most`, or a turn each, or one for up to
 // `alone` turns
@@ -366,28 +444,45 @@ uint32_t grid_of(uint32_t rows, uint32_t lane_bits, uint32_t waves, uint32_t mos
     return turns <= alone ? 1 : turns < most ? turns : most;
 }
 
+template <bool kF32>
+auto kernel_of(uint32_t vec) {
+    return vec == 1   ? balance_kernel<kF32, 1>
+           : vec == 2 ? balance_kernel<kF32, 2>
+           : vec == 3 ? balance_kernel<kF32, 3>
+                      : balance_kernel<kF32, kF32 ? 4 : 3>;
+}
+template <bool kF32>
+auto grad_kernel_of(uint32_t vec) {
+    return vec == 1   ? balance_grad_kernel<kF32, 1>
+           : vec == 2 ? balance_grad_kernel<kF32, 2>
+           : vec == 3 ? balance_grad_kernel<kF32, 3>
+                      : balance_grad_kernel<kF32, kF32 ? 4 : 3>;
+}
+
 }  // namespace
 
 hipError_t launch_balance(BalanceArgs a, bool f32, hipStream_t stream) {
-    a.lane_bits = lane_bits_of(a.experts, f32);
-    const uint32_t grid =
-        grid_of(a.rows, a.lane_bits, kBalanceThreads / 64, kBalanceGrid, kBalanceAlone);
-    auto *kernel = f32 ? (a.experts <= 256   ? balance_kernel<true, 1>
-                          : a.experts <= 512 ? balance_kernel<true, 2>
-                                             : balance_kernel<true, 4>)
-                       : (a.experts <= 512 ? balance_kernel<false, 1> : balance_kernel<false, 2>);
-    return launch_one(kernel, grid, kBalanceThreads, a, 0, stream);
+    constexpr uint32_t kGroupWaves = kBalanceThreads / 64;
+    const uint32_t pieces = pieces_of(a.experts, f32);
+    Hold hold = fewest_lanes(pieces, f32);
+    if (grid_of(a.rows, hold.bits, kGroupWaves, kBalanceGrid, kBalanceAlone) > 1)
+        hold = more_lanes(hold, pieces, a.rows, kBalanceGrid * kBalanceThreads);
+    a.lane_bits = hold.bits;
+    const uint32_t grid = grid_of(a.rows, hold.bits, kGroupWaves, kBalanceGrid, kBalanceAlone);
+    return launch_one(f32 ? kernel_of<true>(hold.vec) : kernel_of<false>(hold.vec), grid,
+                      kBalanceThreads, a, 0, stream);
 }
 
 hipError_t launch_balance_backward(BalanceGradArgs a, bool f32, hipStream_t stream) {
-    a.lane_bits = lane_bits_of(a.experts, f32);
-    const uint32_t grid = grid_of(a.rows, a.lane_bits, kWaves, kBalanceGradGrid, 1);
-    auto *kernel =
-        f32 ? (a.experts <= 256   ? balance_grad_kernel<true, 1>
-               : a.experts <= 512 ? balance_grad_kernel<true, 2>
-                                  : balance_grad_kernel<true, 4>)
-            : (a.experts <= 512 ? balance_grad_kernel<false, 1> : balance_grad_kernel<false, 2>);
-    return launch_one(kernel, grid, kThreads, a, 0, stream);
+    const uint32_t pieces = pieces_of(a.experts, f32);
+    Hold hold = fewest_lanes(pieces, f32);
+    // as many workgroups as are resident at once: with more than 8 experts a lane half of them
+    const uint32_t most = kBalanceGradGrid >> (hold.vec * (f32 ? 4 : 8) > 8);
+    hold = more_lanes(hold, pieces, a.rows, most * kThreads);
+    a.lane_bits = hold.bits;
+    const uint32_t grid = grid_of(a.rows, hold.bits, kWaves, most, 1);
+    return launch_one(f32 ? grad_kernel_of<true>(hold.vec) : grad_kernel_of<false>(hold.vec), grid,
+                      kThreads, a, 0, stream);
 }
 
 }  // namespace bf16d

@@ -92,15 +92,15 @@ hipError_t launch_policy_loss(const PolicyArgs &a, hipStream_t stream);
 // ---- balance loss ------------------------------------------------------------------
 // A workgroup of 16 waves for each CU: as many rows in flight as with small ones,
 // and fewer that add to the shared sums at the end (with 512 workgroups 65536 rows of
-// 64 fp32 experts took 19.1 us instead of 14.4).
+// 64 fp32 experts took 16.6 us instead of 11.7).
 constexpr uint32_t kBalanceGrid = 256;
 constexpr uint32_t kBalanceThreads = 1024;
 constexpr uint32_t kBalanceAlone = 4;        // turns that one takes sooner than joining sums
-// of the sums that workgroups add to: 16384 rows of 64 fp32 experts 11.4 us, with one
-// copy 14.4
+// of the sums that workgroups add to: 16384 rows of 64 fp32 experts 9.7 us, with one
+// copy 13.8
 constexpr uint32_t kBalanceCopies = 8;
-// of four waves: as many as are resident at once (65536 rows of 256 bf16 experts 18.0 us,
-// with 1024 19.0, with 4096 20.9)
+// of four waves, where a lane holds up to 8 experts (262144 rows of 64 bf16 experts 15.5 us,
+// with 1024 17.2), else half of them (262144 of 1024: 209 us, with 2048 241)
 constexpr uint32_t kBalanceGradGrid = 2048;
 struct BalanceArgs {
     const void *logits, *chosen;

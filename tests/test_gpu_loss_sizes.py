@@ -118,6 +118,32 @@ def test_policy_loss_by_its_workgroups(n):
 
 
 @pytest.mark.parametrize("kind,rows,experts,choices", [
+    # rows of many tokens on few lanes, of several pieces each ...
+    ("fp32", 16500, 37, 2), ("bf16", 16500, 71, 9), ("bf16", 8300, 137, 3), ("bf16", 8300, 260, 8),
+    ("fp32", 8300, 140, 17), ("fp32", 8300, 253, 4), ("bf16", 4200, 391, 33), ("bf16", 4200, 766, 2),
+    ("fp32", 4200, 500, 6), ("fp32", 300, 1021, 65), ("fp32", 4200, 300, 5), ("bf16", 600, 1020, 3),
+    # ... and the same ones with more
+    ("fp32", 9000, 37, 2), ("bf16", 1100, 71, 9), ("bf16", 4000, 137, 3), ("bf16", 4096, 260, 8),
+    ("fp32", 8192, 253, 4), ("bf16", 4096, 391, 33), ("fp32", 30, 253, 4), ("bf16", 3, 391, 33)])
+def test_balance_by_its_lanes(kind, rows, experts, choices):
+    log(f"balance {kind} {rows}x{experts}")
+    x, chosen, mask = _router(rows, experts, choices, rows, kind)
+    x[rows // 2] = -math.inf
+    op = RouterBalance(rows, experts, DEV, z_coef=0.01)
+    want = ref.balance(x, chosen, mask, 0.01, 0.01)
+    big = torch.full((rows + 2, experts + 3), 7.0, dtype=x.dtype, device=DEV)
+    view = big[1:-1, 2:-1]
+    view.copy_(x)
+    for _ in range(2):
+        op.run(view, chosen.to(DEV), mask=mask.to(DEV))
+        _check_router(op, want, f"{rows}x{experts}")
+    op.backward(view, view, mask=mask.to(DEV))    # in place
+    ref.check(view, want["grad"], want["grad_off"], "grad")
+    view.fill_(7.0)
+    assert (big == 7.0).all()
+
+
+@pytest.mark.parametrize("kind,rows,experts,choices", [
     ("fp32", 255, 64, 8), ("fp32", 257, 64, 8), ("fp32", 1025, 64, 2), ("fp32", 40009, 64, 4),
     ("bf16", 4099, 8, 2), ("bf16", 70001, 8, 1), ("bf16", 130, 520, 9), ("bf16", 5000, 264, 3),
     ("fp32", 66, 1000, 2), ("bf16", 4500, 1024, 2), ("fp32", 5001, 260, 6)])
