@@ -25,6 +25,14 @@ def test_rows_around_a_workgroups_turn(kind, vocab, top):
 
 
 @both_types
+@pytest.mark.parametrize("n,vocab,top", [(65, 70001, 20), (86, 66000, 3), (128, 34001, 9),
+                                         (129, 34001, 9), (200, 49999, 64)])
+def test_alternatives_of_rows_in_parts(kind, n, vocab, top):
+    """As many parts as there are workgroups for, and rows that are not cut."""
+    _one(kind, n, vocab, vocab + n, top=top, grad=False)
+
+
+@both_types
 @pytest.mark.parametrize("n,vocab,top", [(256, 16500, 5), (257, 33003, 20), (300, 40003, 64),
                                          (280, 70001, 1), (255, 33000, 33)])
 def test_alternatives_of_many_rows(kind, n, vocab, top):
