@@ -253,7 +253,8 @@ class PolicyLoss(_Op):
     (bf16d_policy_loss; the formulas are in bf16delta_loss.h).
 
     After a run over n tokens, on the device:
-      grad_logp, grad_entropy : float32, their first n entries
+      grad_logp, grad_entropy : float32, their first n entries (the second one's are 0
+                where entropy_coef is, as in a run without entropies)
       loss    : scale * the weighted sum of the tokens' losses
       weight  : the sum of the weights
       kl, clipped, entropy : weighted means, of r - 1 - ln r, of the tokens whose
@@ -298,8 +299,7 @@ class PolicyLoss(_Op):
                 0 if weights is None else _row(weights, "weights", _F32, n, device),
                 0 if ref_logp is None else _row(ref_logp, "ref_logp", _F32, n, device),
                 0 if entropy is None else _row(entropy, "entropy", _F32, n, device),
-                grad_logp, 0 if entropy is None else grad_entropy, n, low, high, kl_coef,
-                entropy_coef, scale)
+                grad_logp, grad_entropy, n, low, high, kl_coef, entropy_coef, scale)
         self._call(self._fn, "bf16d_policy_loss", self._args)
 
 
