@@ -370,20 +370,65 @@ __device__ __forceinline__ void add_largest(uint64_t &list, TopShared<kCount> &s
 }
 
 // ---- forward ---------------------------------------------------------------------------
+// 2^d for a d of at most 0.  Close to 1 by its distance from it (a series of 2^d - 1), so that
+// shifts of a row that rises all the way lose no more than one shift of the same height.
+__device__ __forceinline__ double shift_by(float d) {
+    const bool near = d > -1.0f / 32;
+    const float less =
+        d * fmaf(d, fmaf(d, fmaf(d, 9.61812911e-3f, 5.55041087e-2f), 0.240226507f), kLn2);
+    return (double)(near ? less : exp2_fast(d)) + (near ? 1.0 : 0.0);
+}
+// The sums of threads of more than kLogprobChain turns, in 64 bits.  In LDS, as they are
+// needed once in so many turns.
+template <uint32_t kBlock>
+struct LongSums {
+    double s[kBlock], w[kBlock];
+    float m[kBlock];
+
+    // takes the thread's sums and leaves their maximum, by which they go on
+    __device__ __forceinline__ void add(Sums &a, bool first, float c) {
+        const uint32_t i = threadIdx.x;
+        double ls = 0.0, lw = 0.0;
+        if (!first) {
+            const float d = (m[i] - reference(a.m)) * c;
+            const double f = shift_by(d);
+            ls = s[i];
+            lw = f * fma((double)fmaxf(d, kNone), ls, w[i]);
+            ls *= f;
+        }
+        s[i] = ls + a.s;
+        w[i] = lw + a.w;
+        m[i] = a.m;
+        a.s = a.w = 0.0f;
+    }
+    __device__ __forceinline__ Sums sums() const {
+        return Sums{m[threadIdx.x], (float)s[threadIdx.x], (float)w[threadIdx.x]};
+    }
+};
+// A row's terms in one chain of fp32 drift where many are alike (in ln S 1e-5 for 131072 logits,
+// 1e-2 for 2^28).  So they are added up by their vectors, those by their turn, the turns
+// to the thread's sums, and these, after kLogprobChain of them (kLong), to LongSums.
 template <bool kF32, bool kEntropy>
 __device__ __forceinline__ void add_turn(Sums &a, const word4 (&v)[4], float m, float c) {
     constexpr int kPer = kF32 ? 4 : 8;
     shift(a, fmaxf(a.m, m), c);
     const float ref = reference(a.m);
+    float s = 0.0f, w = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 4; ++q) {
+        float vs = 0.0f, vw = 0.0f;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const float t = (element<kF32>(v[q], k) - ref) * c;
             const float e = exp2_fast(t);
-            a.s += e;
-            if constexpr (kEntropy) a.w += e * fmaxf(t, kNone);
+            vs = k ? vs + e : e;
+            if constexpr (kEntropy) vw = k ? vw + e * fmaxf(t, kNone) : e * fmaxf(t, kNone);
         }
+        s = q ? s + vs : vs;
+        if constexpr (kEntropy) w = q ? w + vw : vw;
+    }
+    a.s += s;
+    if constexpr (kEntropy) a.w += w;
 }
 
 // The outputs of a row that is left out, or of one whose sums are complete.
@@ -420,11 +465,12 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, uint32_t row, co
     }
 }
 
-template <uint32_t kBlock, bool kF32, bool kEntropy, bool kTop, bool kKeep>
+template <uint32_t kBlock, bool kF32, bool kEntropy, bool kTop, bool kKeep, bool kLong>
 __global__ __launch_bounds__(kBlock, kTop ? 8 : 1) void logprob_kernel(LogprobArgs a) {
     constexpr uint32_t kCount = kBlock / 64;
     __shared__ float s_tmp[kCount][3];
     __shared__ TopShared<kTop ? kCount : 1> s_top;
+    __shared__ LongSums<kLong ? kBlock : 1> s_long;
     constexpr uint32_t kPer = kF32 ? 4 : 8, kSize = kF32 ? 4 : 2;
     const uint32_t row = scalar_div(blockIdx.x, a.parts), part = blockIdx.x - row * a.parts;
     const RowVectors<kF32> r(row_ptr(a.logits, row, a.inner, kSize), a.vocab);
@@ -473,6 +519,13 @@ __global__ __launch_bounds__(kBlock, kTop ? 8 : 1) void logprob_kernel(LogprobAr
             for (int q = 0; q < 4; ++q) v[q] = fresh(v[q]);
         }
         add_turn<kF32, kEntropy>(mine, v, most, a.scale);
+        if constexpr (kLong) {
+            const uint32_t had = turn + 1 - begin;
+            if (had % kLogprobChain == 0 || turn + 1 == end) {
+                s_long.add(mine, had <= kLogprobChain, a.scale);
+                if (turn + 1 == end) mine = s_long.sums();
+            }
+        }
         if constexpr (kWide) {
             if (turn + 1 < end) load(turn + 1);
         }
@@ -608,10 +661,15 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
 
 template <bool kF32, bool kEntropy>
 hipError_t launch_forward(const LogprobArgs &a, bool wide, bool keep, hipStream_t stream) {
-    auto *kernel = a.top  ? logprob_kernel<kLogprobWide, kF32, kEntropy, true, true>
-                   : wide ? logprob_kernel<kLogprobWide, kF32, kEntropy, false, true>
-                   : keep ? logprob_kernel<kThreads, kF32, kEntropy, false, true>
-                          : logprob_kernel<kThreads, kF32, kEntropy, false, false>;
+    // a long row is read with non-temporal loads; a wide one without alternatives is not long
+    const bool lengthy = a.part_turns > kLogprobChain;
+    auto *kernel =
+        a.top ? (lengthy ? logprob_kernel<kLogprobWide, kF32, kEntropy, true, true, true>
+                         : logprob_kernel<kLogprobWide, kF32, kEntropy, true, true, false>)
+        : wide    ? logprob_kernel<kLogprobWide, kF32, kEntropy, false, true, false>
+        : lengthy ? logprob_kernel<kThreads, kF32, kEntropy, false, false, true>
+        : keep    ? logprob_kernel<kThreads, kF32, kEntropy, false, true, false>
+                  : logprob_kernel<kThreads, kF32, kEntropy, false, false, false>;
     return launch_one(kernel, a.rows * a.parts, wide ? kLogprobWide : kThreads, a, 0, stream);
 }
 

@@ -1,0 +1,187 @@
+"""The losses over the longest axes that they take: rows of up to 2^28 logits, whose sums
+have to keep their digits, routers of up to 2^24 tokens, and a gradient of more
+turns than a grid has workgroups.
+
+The bounds are those of tests/loss_reference.py with a number of sums, N, that does not
+grow with a row."""
+import math
+
+import pytest
+import torch
+
+from lossless_bf16_weight_xor_amd import TokenLogProbs
+from tests import loss_reference as ref
+from tests.gpu_util import log
+from tests.test_gpu_loss import DEV, TYPES, both_types
+
+pytestmark = pytest.mark.gpu
+U = ref.U
+
+# Sums that a term of a row passes, each adding u: its vector's (7 in bf16) and its turn's (3),
+# those of 32 turns, then 64 bits; to 32 bits (1); the lanes, the waves and the parts, as
+# often again for rows in parts (2 x 10 + 1), with five shifts of 3u there; 6 for the term's own
+# exponential and the results.
+N = 7 + 3 + 32 + 1 + 21 + 15 + 6
+# A shift of the sums in 64 bits has an error in proportion to its distance (the product and
+# its coefficient 3u, the series 4u), and the distances add up to |d|.
+SHIFT = 8
+
+
+def _zeros(vocab):
+    """Where the maximum is: 8192 elements of every 2^19, so that a sum begins there and
+    the terms that follow are not 1."""
+    return (torch.arange(vocab) // 8192) % 64 == 0
+
+
+def _two_values(value, zeros, others, temperature):
+    """(ln S, H, and the bounds of both) of a row of so many logits 0 and others of `value`,
+    in 64 bits; s, q as in tests/loss_reference.py."""
+    d = value / temperature
+    s = zeros + others * math.exp(d)
+    p = others * math.exp(d) / s
+    q, ln_s = p * -d, math.log(s)
+    s_off = U * (SHIFT * q + N + 3)
+    ln_off = s_off + 2 * U * ln_s
+    h_off = 1.01 * (ln_off + SHIFT * U * p * d * d + q * (2 * s_off + U * (N + 8))
+                    + 2 * U * (ln_s + q))
+    return ln_s, ln_s + q, 1.01 * ln_off, h_off
+
+
+# 32000 and 131072: ordinary ones; 2^20 + 5 and 2^24 whole and in parts; and, in one row whose
+# memory all tokens share, the longest that a call takes
+@both_types
+@pytest.mark.parametrize("vocab,inner", [(32000, 64), (131072, 64), ((1 << 20) + 5, 64),
+                                         ((1 << 20) + 5, 4), (1 << 24, 33), (1 << 24, 5),
+                                         (1 << 28, 33)])
+def test_sums_of_equal_logits(kind, vocab, inner):
+    """Terms that are all alike are rounded alike: a sum that takes them one by one drifts."""
+    log(f"{kind} {vocab} x {inner}")
+    rows = 1 if vocab == 1 << 28 else 8
+    values = torch.tensor([-0.3, -0.7, -1.1, -1.3, -1.7, -2.1, -2.7, -3.3])[-rows:].to(TYPES[kind])
+    inner = inner * 8 // rows
+    zero = _zeros(vocab)
+    zeros = int(zero.sum())
+    x = values.to(DEV)[:, None].repeat(1, vocab)
+    x[:, zero.to(DEV)] = 0.0
+    y = torch.tensor([0, 8200, vocab // 2, vocab - 1]).repeat(inner)[:inner]
+    op = TokenLogProbs(rows * inner, vocab, DEV, entropy=True)
+    for temperature in (1.0, 0.7):
+        op.run(x[:, None, :].expand(rows, inner, vocab), y.to(DEV).expand(rows, inner),
+               temperature)
+        logp, entropy = op.logp.view(rows, inner).cpu(), op.entropy.view(rows, inner).cpu()
+        for row, value in enumerate(values.tolist()):
+            ln_s, h, ln_off, h_off = _two_values(value, zeros, vocab - zeros, temperature)
+            d = torch.zeros(inner, dtype=ref.F64).masked_fill(~zero[y], value / temperature)
+            want = d - ln_s
+            ref.check(logp[row], want, ln_off + 1.01 * U * (3 * d.abs() + want.abs()),
+                      f"logp of {value}")
+            ref.check(entropy[row], torch.full((inner,), h, dtype=ref.F64), h_off,
+                      f"entropy of {value}")
+
+
+@both_types
+def test_the_gradient_of_equal_logits(kind):
+    """The sums' error is that of every element of a gradient."""
+    log(f"{kind} gradient")
+    vocab, inner = (1 << 20) + 5, 300
+    value = torch.tensor(-1.3).to(TYPES[kind]).item()
+    zero = _zeros(vocab)
+    zeros = int(zero.sum())
+    x = torch.full((1, vocab), value, dtype=TYPES[kind], device=DEV)
+    x[:, zero.to(DEV)] = 0.0
+    y = torch.full((inner,), 9, device=DEV)
+    op = TokenLogProbs(inner, vocab, DEV, entropy=True)
+    op.run(x.expand(inner, vocab), y)
+    out = torch.empty(inner, vocab, dtype=x.dtype, device=DEV)
+    a = torch.linspace(-1.0, 1.0, inner, device=DEV)
+    op.backward(x.expand(inner, vocab), y, a, out)
+    ln_s, _, ln_off, _ = _two_values(value, zeros, vocab - zeros, 1.0)
+    half = ref.BF16 if kind == "bf16" else U
+    for j in (0, 8, 10, 8200, vocab // 2 - 1, vocab - 1):
+        d = 0.0 if zero[j] else value
+        off = ln_off + U * (3 * abs(d) + 8 + abs(d - ln_s)) + half
+        want = -a.cpu().double() * math.exp(d - ln_s)
+        ref.check(out[:, j], want, want.abs() * off * 1.01 + ref.TINY, f"element {j}")
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("rise", [0.25, 1.0, 30.0, 3000.0])
+def test_sums_of_a_row_that_rises(whole, rise):
+    """Every turn has a new maximum, by which all sums before are shifted."""
+    vocab, n = (1 << 23) + 3, 260 if whole else 5
+    log(f"rises by {rise}, {n} rows")
+    x = torch.linspace(0.0, rise, vocab)
+    y = torch.tensor([vocab - 1])
+    op = TokenLogProbs(n, vocab, DEV, entropy=True)
+    op.run(x.to(DEV).expand(n, vocab), y.to(DEV).expand(n))
+    d = x.double() - x[-1].double()
+    p = d.exp()
+    s = p.sum()
+    p /= s
+    q, ln_s = (p * -d).sum(), s.log()
+    s_off = U * (SHIFT * q + N + 3)
+    # the shifts within 32 turns, and those of more than 1/32 in the logarithm to 2 of
+    # what is left of the sums in 64 bits: 3u each
+    s_off += 3 * U * (32 + 1 / (1 - 2 ** -(1 / 32)))
+    ln_off = 1.01 * (s_off + 2 * U * ln_s)
+    ref.check(op.logp, -ln_s.expand(n), ln_off, "logp")
+    h_off = 1.01 * (ln_off + SHIFT * U * (p * d * d).sum() + q * (2 * s_off + U * (N + 8))
+                    + 2 * U * (ln_s + q))
+    ref.check(op.entropy, (ln_s + q).expand(n), h_off, "entropy")
+
+
+@both_types
+def test_sums_of_equal_logits_with_alternatives(kind):
+    log(f"{kind} alternatives")
+    vocab, n, value = (1 << 21) + 5, 130, -0.75
+    zero = _zeros(vocab)
+    zeros = int(zero.sum())
+    x = torch.full((1, vocab), value, dtype=TYPES[kind], device=DEV)
+    x[:, zero.to(DEV)] = 0.0
+    y = torch.full((n,), vocab - 1, device=DEV)      # a zero, too
+    op = TokenLogProbs(n, vocab, DEV, entropy=True, top=60)
+    op.run(x.expand(n, vocab), y)
+    ln_s, h, ln_off, h_off = _two_values(value, zeros, vocab - zeros, 1.0)
+    want = torch.full((n,), -ln_s, dtype=ref.F64)
+    ref.check(op.logp, want, ln_off + 1.01 * U * ln_s, "logp")
+    ref.check(op.entropy, torch.full((n,), h, dtype=ref.F64), h_off, "entropy")
+    assert torch.equal(op.top_ids.cpu(), torch.arange(60).expand(n, 60))
+    ref.check(op.top_logp, torch.full((n, 60), -ln_s, dtype=ref.F64), ln_off + U * ln_s, "top")
+
+
+@both_types
+@pytest.mark.parametrize("vocab,top", [((1 << 19) + 3, 0), ((1 << 21) + 3, 2)])
+def test_long_rows_that_are_special(kind, vocab, top):
+    """Nothing but -infinity, in all turns or in the first ones; NaN and infinity early and
+    late; the lowest value; rows that are left out."""
+    log(f"{kind} {vocab}")
+    low, inf = torch.finfo(TYPES[kind]).min, math.inf
+    x = torch.full((9, vocab), -0.75, dtype=TYPES[kind])
+    x[0] = -inf
+    x[1, :-1] = -inf            # all weight on the last element
+    x[2, : vocab // 2] = -inf
+    x[3, vocab // 2:] = -inf
+    x[4, 5] = math.nan
+    x[5, -1] = math.nan
+    x[6, -1] = inf
+    x[7] = low
+    y = torch.full((9,), vocab - 1)
+    y[8] = -1
+    inner = 29
+    op = TokenLogProbs(9 * inner, vocab, DEV, entropy=True, top=top)
+    op.run(x.to(DEV)[:, None, :].expand(9, inner, vocab), y.to(DEV)[:, None].expand(9, inner))
+    logp, entropy = op.logp.view(9, inner).cpu(), op.entropy.view(9, inner).cpu()
+    assert (logp[0] == -inf).all() and (entropy[0] == 0).all()
+    assert (logp[1] == 0).all() and (entropy[1] == 0).all()
+    for row, count in ((2, vocab - vocab // 2), (3, vocab // 2), (7, vocab)):
+        ln_s, h, ln_off, h_off = _two_values(-1.0, count, 0, 1.0)
+        off = torch.full((inner,), h_off, dtype=ref.F64)
+        ref.check(entropy[row], torch.full((inner,), h, dtype=ref.F64), off, f"entropy {row}")
+        want = torch.full((inner,), -inf if row == 3 else -ln_s, dtype=ref.F64)
+        ref.check(logp[row], want, ln_off + 1.01 * U * ln_s, f"logp {row}")
+    assert logp[4:7].isnan().all() and entropy[4:7].isnan().all()
+    assert (logp[8] == 0).all() and (entropy[8] == 0).all()
+    if top:
+        ids = op.top_ids.view(9, inner, top)[:, 0].tolist()
+        assert ids[0] == ids[8] == [-1, -1] and ids[1] == [vocab - 1, -1]
+        assert ids[2] == [vocab // 2, vocab // 2 + 1] and ids[3] == ids[7] == [0, 1]
