@@ -1,6 +1,8 @@
 """Results of the losses' objects over calls of different kinds: a run without entropies
 after one with them, ratios far from 1, another number of rows, and gradients over
 tensors that an autograd graph has saved."""
+import math
+
 import pytest
 import torch
 
@@ -31,3 +33,39 @@ def test_the_entropies_gradient_after_a_run_without_them(n):
     probs.backward(x, y, op.grad_logp[:n], got, grad_entropy=op.grad_entropy[:n])
     probs.backward(x, y, op.grad_logp[:n], want, grad_entropy=torch.zeros(n, device=DEV))
     assert torch.equal(got, want)
+
+
+def test_ratios_far_below_one():
+    """An unclipped ratio keeps its digits down to the smallest that fp32 holds."""
+    log("far ratios")
+    u = torch.cat([-torch.arange(0, 104, 0.25), -1.0 + torch.linspace(-0.01, 0.01, 99)])
+    n = u.numel()
+    for old in (-0.5, 0.0, -37.125):
+        s = dict(logp=u + old, old=torch.full((n,), old), adv=torch.full((n,), 1.7))
+        op = PolicyLoss(n, DEV)
+        want = _policy(op, s, f"old {old}")          # to one rounding
+        assert (op.grad_logp[:n].cpu()[want["grad_logp"] < -2.0 ** -149] < 0).all()
+        # with a factor that lifts them into the range of fp32's normal numbers
+        _policy(op, s, f"old {old} scaled", scale=1e30)
+
+
+def test_ratios_over_the_whole_range():
+    """Ratios, and distances from a reference, between and around the halves of ln 2, next
+    to 1, far above, and beyond the range of 64 bits."""
+    log("whole range")
+    half = math.log(2.0) / 2
+    steps = torch.cat([torch.arange(-600, 241) * half, torch.arange(-400, 400) * 1e-9,
+                       10.0 ** torch.arange(-30, -1, dtype=torch.float32)])
+    u = torch.cat([steps, torch.nextafter(steps, steps + 1), torch.nextafter(steps, steps - 1)])
+    n, zero = u.numel(), torch.zeros(u.numel())
+    op = PolicyLoss(n, DEV)
+    s = dict(logp=u, old=zero, adv=torch.where(u > 0, -1.0, 1.0))        # none is clipped
+    want = _policy(op, s, "ratios", scale=1e-30)
+    assert want["clipped"] == 0
+    _policy(op, dict(logp=zero, old=zero, adv=zero, ref=u), "reference", kl_coef=0.7, scale=1e-30)
+    for far in (750.0, 1e5, 3e38, math.inf):
+        for sign in (1.0, -1.0):
+            one = torch.tensor([far * sign])
+            _policy(op, dict(logp=one, old=zero[:1], adv=torch.tensor([-sign])), f"{one}")
+            _policy(op, dict(logp=zero[:1], old=zero[:1], adv=zero[:1], ref=one), f"ref {one}",
+                    kl_coef=1.0)
