@@ -148,7 +148,8 @@ struct RowSoftmax {
     __device__ __forceinline__ float lse() const { return m + kLn2 * __builtin_amdgcn_logf(sum); }
 };
 
-template <bool kF32, int kVec>
+// kLong: waves of more than kBalanceChain turns.
+template <bool kF32, int kVec, bool kLong>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a) {
     constexpr int kPer = kF32 ? 4 : 8;
     constexpr uint32_t kGroupWaves = kBalanceThreads / 64;
@@ -187,9 +188,53 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         if (id >= (int64_t)a.experts) bad_id = true;
         else if (id >= 0) atomicAdd(&s_words[id], 1ull);
     };
+    // The lane's sums of p, as integers to the workgroup's.
+    // Rows of up to 16 lanes: the sums of a wave's four quarters are added up first, and
+    // each quarter hands over a fourth of them.
+    const uint32_t quarter = lane >> 4;
+    auto add_p = [&](int v, uint32_t k, float x, float weight) {
+        if (weight != 0.0f && x > 0.0f && x < INFINITY)
+            atomicAdd(&s_words[a.experts + P.start[v] + k],
+                      (unsigned long long)__double2ll_rn((double)x * kFixed));
+    };
+    auto weight = [&](int v, int k) { return v < kVec - 1 ? 1.0f : P.weight[k]; };
+    auto hand_over_p = [&] {
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+#pragma unroll
+            for (int k = 0; k < kPer; k += 4) {
+                if (P.bits > 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) add_p(v, k + j, p[v][k + j], weight(v, k + j));
+                    continue;
+                }
+                float x = 0.0f, of = 0.0f;
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) {
+                    float even, odd;
+                    both_halves<32>(p[v][k + j], even, odd);
+                    both_halves<16>(even + odd, even, odd);
+                    x = quarter == j ? even + odd : x;
+                    of = quarter == j ? weight(v, k + j) : of;
+                }
+                add_p(v, k + quarter, x, of);
+            }
+    };
     if (base < a.rows) fetch(row);   // while the sums are cleared
     clear();
+    uint32_t had = 0;   // turns
     for (uint32_t at = base; at < a.rows; at += step, row += step) {   // a wave's rows
+        if constexpr (kLong) {
+            if (had == kBalanceChain) {
+                hand_over_p();
+#pragma unroll
+                for (int v = 0; v < kVec; ++v)
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) p[v][k] = 0.0f;
+                had = 0;
+            }
+            ++had;
+        }
         Turn<kF32, kVec> now = next;
         const int64_t id = next_id;
         if (at + step < a.rows) fetch(row + step);
@@ -213,35 +258,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     if (tokens) atomicAdd(&s_more[kSumTokens], (unsigned long long)tokens);
     if (bad_id) s_more[kSumBadIds] = 1;
     if (bad_row) s_more[kSumBadRows] = 1;
-    // Rows of up to 16 lanes: the sums of a wave's four quarters are added up first, and
-    // each quarter hands over a fourth of them.
-    const uint32_t quarter = lane >> 4;
-    auto add_p = [&](int v, uint32_t k, float x, float weight) {
-        if (weight != 0.0f && x > 0.0f && x < INFINITY)
-            atomicAdd(&s_words[a.experts + P.start[v] + k],
-                      (unsigned long long)__double2ll_rn((double)x * kFixed));
-    };
-    auto weight = [&](int v, int k) { return v < kVec - 1 ? 1.0f : P.weight[k]; };
-#pragma unroll
-    for (int v = 0; v < kVec; ++v)
-#pragma unroll
-        for (int k = 0; k < kPer; k += 4) {
-            if (P.bits > 4) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) add_p(v, k + j, p[v][k + j], weight(v, k + j));
-                continue;
-            }
-            float x = 0.0f, of = 0.0f;
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                float even, odd;
-                both_halves<32>(p[v][k + j], even, odd);
-                both_halves<16>(even + odd, even, odd);
-                x = quarter == j ? even + odd : x;
-                of = quarter == j ? weight(v, k + j) : of;
-            }
-            add_p(v, k + quarter, x, of);
-        }
+    hand_over_p();
     // sums over the workgroup, a value a lane, in a fixed order
     auto totals = [&](double (&x)[3]) {
 #pragma unroll
@@ -444,12 +461,12 @@ uint32_t grid_of(uint32_t rows, uint32_t lane_bits, uint32_t waves, uint32_t mos
     return turns <= alone ? 1 : turns < most ? turns : most;
 }
 
-template <bool kF32>
+template <bool kF32, bool kLong>
 auto kernel_of(uint32_t vec) {
-    return vec == 1   ? balance_kernel<kF32, 1>
-           : vec == 2 ? balance_kernel<kF32, 2>
-           : vec == 3 ? balance_kernel<kF32, 3>
-                      : balance_kernel<kF32, kF32 ? 4 : 3>;
+    return vec == 1   ? balance_kernel<kF32, 1, kLong>
+           : vec == 2 ? balance_kernel<kF32, 2, kLong>
+           : vec == 3 ? balance_kernel<kF32, 3, kLong>
+                      : balance_kernel<kF32, kF32 ? 4 : 3, kLong>;
 }
 template <bool kF32>
 auto grad_kernel_of(uint32_t vec) {
@@ -469,8 +486,12 @@ hipError_t launch_balance(BalanceArgs a, bool f32, hipStream_t stream) {
         hold = more_lanes(hold, pieces, a.rows, kBalanceGrid * kBalanceThreads);
     a.lane_bits = hold.bits;
     const uint32_t grid = grid_of(a.rows, hold.bits, kGroupWaves, kBalanceGrid, kBalanceAlone);
-    return launch_one(f32 ? kernel_of<true>(hold.vec) : kernel_of<false>(hold.vec), grid,
-                      kBalanceThreads, a, 0, stream);
+    const uint64_t chain = (uint64_t)grid * kGroupWaves * (64u >> hold.bits) * kBalanceChain;
+    auto *kernel = a.rows > chain
+                       ? (f32 ? kernel_of<true, true>(hold.vec) : kernel_of<false, true>(hold.vec))
+                       : f32 ? kernel_of<true, false>(hold.vec)
+                             : kernel_of<false, false>(hold.vec);
+    return launch_one(kernel, grid, kBalanceThreads, a, 0, stream);
 }
 
 hipError_t launch_balance_backward(BalanceGradArgs a, bool f32, hipStream_t stream) {

@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from lossless_bf16_weight_xor_amd import TokenLogProbs
+from lossless_bf16_weight_xor_amd import RouterBalance, TokenLogProbs
 from tests import loss_reference as ref
 from tests.gpu_util import log
 from tests.test_gpu_loss import DEV, TYPES, both_types
@@ -185,3 +185,62 @@ def test_long_rows_that_are_special(kind, vocab, top):
         ids = op.top_ids.view(9, inner, top)[:, 0].tolist()
         assert ids[0] == ids[8] == [-1, -1] and ids[1] == [vocab - 1, -1]
         assert ids[2] == [vocab // 2, vocab // 2 + 1] and ids[3] == ids[7] == [0, 1]
+
+
+@pytest.mark.parametrize("kind,experts", [("bf16", 1024), ("fp32", 1021), ("fp32", 513),
+                                          ("bf16", 40)])
+def test_sums_of_very_many_tokens(kind, experts):
+    """2^24 - 1 tokens that share a row: each expert's probabilities, all alike, add up."""
+    rows = (1 << 24) - 1
+    log(f"{kind} {rows}x{experts}")
+    x = torch.zeros(1, experts, dtype=TYPES[kind])
+    x[0, ::3] = -0.7
+    x[0, 5] = 1.3
+    d = x[0].double() - x[0].double().max()
+    s = d.exp().sum()
+    lse = x[0].double().max() + s.log()
+    p = d.exp() / s
+    op = RouterBalance(rows, experts, DEV, z_coef=0.01)
+    for e in (0, 1, 5, experts - 1):
+        chosen = torch.tensor([[e]], device=DEV)
+        op.run(x.to(DEV).expand(rows, experts), chosen.expand(rows, 1))
+        assert op.tokens == rows and op.counts[e] == rows and op.counts.sum() == rows
+        # p: tests/loss_reference.py; 64 sums of a lane before it hands them over, two
+        # joins of lanes; a step of 2^-37 for each time, a row at least; the result
+        p_off = U * (3 * d[e].abs() + 3 * (p * d.abs()).sum() + 9 + math.log2(experts))
+        off = p[e] * (p_off + U * (64 + 2 + 1)) + 2.0 ** -37
+        ref.check(op.balance, experts * p[e], 1.01 * experts * off, f"balance of {e}")
+        lse_off = U * (3 * (p * d.abs()).sum() + 4 + math.log2(experts) + 3 * s.log() + lse.abs())
+        ref.check(op.z, lse ** 2, 1.01 * 2 * lse * lse_off + 2 * U * lse ** 2, "z")
+
+
+@both_types
+@pytest.mark.parametrize("rows,experts", [(600000, 520), (2200001, 40)])
+def test_tokens_of_more_turns_than_a_lane_adds_up(kind, rows, experts):
+    """Different rows, the last turns short; a wave that ends within its second 64 turns."""
+    log(f"{kind} {rows}x{experts}")
+    g = torch.Generator(DEV)
+    g.manual_seed(rows)
+    x = torch.randn(rows, experts, generator=g, device=DEV).to(TYPES[kind])
+    chosen = torch.randint(0, experts, (rows, 2), generator=g, device=DEV)
+    mask = torch.rand(rows, generator=g, device=DEV) > 0.1
+    op = RouterBalance(rows, experts, DEV, z_coef=0.01)
+    op.run(x, chosen, mask=mask)
+    p = torch.zeros(experts, dtype=ref.F64, device=DEV)
+    z = 0.0
+    for a in range(0, rows, 1 << 17):
+        live = mask[a:a + (1 << 17)]
+        y = x[a:a + (1 << 17)][live].double()
+        p += y.softmax(1).sum(0)
+        z += y.logsumexp(1).square().sum().item()
+    counts = torch.bincount(chosen[mask].flatten(), minlength=experts)
+    n = int(mask.sum())
+    assert torch.equal(op.counts, counts) and op.tokens == n
+    want = (experts * (counts.double() / counts.sum() * p).sum() / n).cpu()
+    # |d| of normal numbers stays below 12, its mean by p below 6
+    off = U * (3 * 12 + 3 * 6 + 9 + math.log2(experts) + 64 + 2 + 1)
+    ref.check(op.balance, want, 1.01 * (off * want + experts * 2.0 ** -37), "balance")
+    lse = 12.0                     # and ln of the sum of e^x
+    lse_off = U * (3 * 6 + 4 + math.log2(experts) + 3 * lse + lse)
+    want = torch.tensor(z / n, dtype=ref.F64)
+    ref.check(op.z, want, 1.01 * 2 * want.sqrt() * lse_off + 2 * U * want, "z")
