@@ -331,7 +331,7 @@ class RouterBalance(_Op):
             ((self.experts,), torch.int64), ((4,), torch.int64), ((size,), torch.uint8))
         self.loss, self.balance, self.z = self.result.view(torch.float32)[:3].unbind()
         self.tokens = self.result[2]
-        self._ran = False
+        self._ran = None    # rows of the last run
         self._coefs = float(balance_coef), float(z_coef)
         self._job = _native.BalanceJob(balance_coef=balance_coef, z_coef=z_coef,
                                        counts=self.counts.data_ptr())
@@ -379,15 +379,15 @@ class RouterBalance(_Op):
         _BALANCE(self._job, 0, x, chosen.data_ptr(), seen, n, stride, chosen_stride,
                  self.experts, choices, kind, ids)
         self._call(self._fn, "bf16d_balance", self._args)
-        self._ran = True
+        self._ran = n
 
     def backward(self, logits: torch.Tensor, out: torch.Tensor, mask: torch.Tensor | None = None,
                  scale: float = 1.0) -> None:
         """scale * the gradient of the loss by the logits, into `out` (their type and shape;
         the logits themselves are fine).  logits, mask: those of the last run."""
-        if not self._ran:
-            raise ValueError("backward needs the counts of a run")
         n, shape, kind, x, stride, seen = self._rows_of(logits, mask)
+        if n != self._ran:
+            raise ValueError(f"{n} rows, but the last run had {self._ran}: backward needs its counts")
         if not (isinstance(out, torch.Tensor) and out.get_device() == self._index
                 and out.dtype == logits.dtype and out.shape == shape):
             _refuse(out, "out", (logits.dtype,), shape, self.device)

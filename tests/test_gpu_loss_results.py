@@ -6,7 +6,8 @@ import math
 import pytest
 import torch
 
-from lossless_bf16_weight_xor_amd import PolicyLoss, TokenLogProbs
+from lossless_bf16_weight_xor_amd import PolicyLoss, RouterBalance, TokenLogProbs
+from tests import loss_reference as ref
 from tests.gpu_util import log
 from tests.test_gpu_loss import DEV, _policy, _policy_inputs
 
@@ -69,3 +70,22 @@ def test_ratios_over_the_whole_range():
             _policy(op, dict(logp=one, old=zero[:1], adv=torch.tensor([-sign])), f"{one}")
             _policy(op, dict(logp=zero[:1], old=zero[:1], adv=zero[:1], ref=one), f"ref {one}",
                     kl_coef=1.0)
+
+
+def test_a_routers_gradient_of_other_rows_is_refused():
+    log("other rows")
+    x = torch.randn(6, 8, device=DEV)
+    ids = torch.zeros(6, 2, dtype=torch.int64, device=DEV)
+    op = RouterBalance(6, 8, DEV)
+    op.run(x, ids)
+    for rows in (5, 0):
+        with pytest.raises(ValueError, match="last run had 6"):
+            op.backward(x[:rows], torch.empty_like(x[:rows]))
+    op.run(x[:5], ids[:5])
+    with pytest.raises(ValueError, match="last run had 5"):
+        op.backward(x, torch.empty_like(x))
+    out = torch.full_like(x, 7.0)
+    op.backward(x[:5], out[:5])
+    want = ref.balance(x[:5].cpu(), ids[:5].cpu())
+    ref.check(out[:5], want["grad"], want["grad_off"], "grad")
+    assert (out[5] == 7.0).all()
