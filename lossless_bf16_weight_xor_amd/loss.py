@@ -15,7 +15,9 @@ Every call enqueues one kernel on the current stream and nothing else, and may b
 captured into a graph (keep the object and the tensors alive as long as it).  Results
 stay on the device, in buffers of the object that its next run overwrites.  Calls
 of one object must not overlap in time, nor replays of graphs that hold them.
-Tensors that are passed in stay their owner's, as in any torch call.
+Tensors that are passed in stay their owner's, as in any torch call.  A backward call
+records nothing in an autograd graph; it counts as an in-place write of `out`, so that a
+graph which has saved those logits for its own backward refuses to use their gradient.
 """
 from __future__ import annotations
 
@@ -25,6 +27,7 @@ import math
 import struct
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _native
 from . import _check_rc
@@ -246,6 +249,7 @@ class TokenLogProbs(_Op):
                       out.data_ptr(), strides[0] if len(strides) == 3 else 0, strides[-2], outer,
                       inner, self.vocab, kind, ids, 0, self._stats, a, h)
         self._call(self._grad_fn, "bf16d_logprob_backward", self._grad_args)
+        increment_version(out)
 
 
 class PolicyLoss(_Op):
@@ -397,3 +401,4 @@ class RouterBalance(_Op):
         _BALANCE_GRAD(self._grad_job, 0, x, out.data_ptr(), seen, n, stride, out_stride,
                       self.experts, kind, *self._coefs, scale)
         self._call(self._grad_fn, "bf16d_balance_backward", self._grad_args)
+        increment_version(out)

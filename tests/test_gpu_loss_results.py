@@ -89,3 +89,40 @@ def test_a_routers_gradient_of_other_rows_is_refused():
     want = ref.balance(x[:5].cpu(), ids[:5].cpu())
     ref.check(out[:5], want["grad"], want["grad_off"], "grad")
     assert (out[5] == 7.0).all()
+
+
+def test_a_graph_that_saved_the_logits_sees_their_gradient_over_them():
+    """backward() counts as a write of `out`: autograd refuses to use what it has saved of
+    it, instead of taking the gradient for the logits."""
+    log("saved logits")
+    weight = torch.randn(16, 40, device=DEV, requires_grad=True)
+    states = torch.randn(6, 16, device=DEV)
+    y = torch.arange(6, device=DEV)
+    a = torch.ones(6, device=DEV)
+    probs, router = TokenLogProbs(6, 40, DEV), RouterBalance(6, 40, DEV)
+
+    def calls():
+        yield lambda x: (probs.run(x, y), probs.backward(x, y, a, out=x))
+        yield lambda x: (router.run(x, y[:, None]), router.backward(x, x))
+
+    for call in calls():
+        logits = states @ weight
+        saved = logits.square().sum()        # keeps the logits for its backward
+        call(logits.detach())                # the same memory
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.backward()
+        # beside the logits nothing is in the way, nor in a graph that has not saved them
+        logits = states @ weight
+        saved, linear = logits.square().sum(), logits.sum()
+        out = torch.empty_like(logits)
+        before = out._version, logits._version
+        call_out = (lambda x: (probs.run(x, y), probs.backward(x, y, a, out=out)))
+        call_out(logits.detach())
+        assert out._version > before[0] and logits._version == before[1]
+        (saved + linear).backward()
+    # tensors without a counter are fine
+    with torch.inference_mode():
+        x = states @ weight
+        for call in calls():
+            call(x.clone())
+    torch.cuda.synchronize()
