@@ -244,3 +244,67 @@ def test_tokens_of_more_turns_than_a_lane_adds_up(kind, rows, experts):
     lse_off = U * (3 * 6 + 4 + math.log2(experts) + 3 * lse + lse)
     want = torch.tensor(z / n, dtype=ref.F64)
     ref.check(op.z, want, 1.01 * 2 * want.sqrt() * lse_off + 2 * U * want, "z")
+
+
+def test_a_gradient_of_more_turns_than_a_grid_has_workgroups():
+    """2^24 / 3 rows of three turns: a workgroup takes two of them, the last one of a
+    row one.  183 GB are written; the logits and their stats are of a few rows each."""
+    rows, vocab, kinds = ((1 << 24) // 3) // 7 * 7 + 7, 16385, 7
+    size = 2 * rows * vocab
+    assert 3 * rows > (1 << 24)
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    if free < size + (8 << 30):
+        pytest.skip(f"needs {size >> 30} GiB, {free >> 30} are free")
+    log(f"{rows} rows of {vocab}, {size >> 30} GiB")
+    g = torch.Generator().manual_seed(0)
+    x = (2 * torch.randn(1, vocab, generator=g)).to(torch.bfloat16)
+    y = torch.tensor([0, 8191, 8192, 16383, 16384, -1, 77])
+    a = torch.randn(kinds, generator=g)
+    op = TokenLogProbs(rows, vocab, DEV)
+    logits, tokens = x.to(DEV).expand(rows, vocab), y.to(DEV).repeat(rows // kinds)
+    op.run(logits, tokens)
+    live = y >= 0
+    want = ref.Rows(x.expand(int(live.sum()), vocab), y[live])
+    ref.check(op.logp[:kinds][live.to(DEV)], want.logp, want.logp_off, "logp")
+    assert (op.logp.view(-1, kinds) == op.logp[:kinds]).all()
+    log("gradient")
+    out = torch.empty(rows, vocab, dtype=torch.bfloat16, device=DEV)
+    op.backward(logits, tokens, a.to(DEV).repeat(rows // kinds), out)
+    grad, off = want.grad(a[live], None, torch.bfloat16)
+    ref.check(out[:kinds][live.to(DEV)], grad, off, "grad")
+    assert (out[5] == 0).all()
+    # rows of the same kind have the same bits
+    bits = out.view(torch.int16).view(-1, kinds, vocab)
+    step = 1 << 15
+    for first in range(0, rows // kinds, step):
+        assert (bits[first:first + step] == bits[0]).all(), first
+    del bits, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows,top", [((1 << 24) - 1, 0), ((1 << 22) - 1, 2)])
+def test_the_most_rows_of_a_call(rows, top):
+    """As many workgroups as a grid's 2^32 threads allow, of 4 waves and of 16."""
+    log(f"{rows} rows, top {top}")
+    vocab, kinds = 5, 1 << 20
+    g = torch.Generator().manual_seed(top)
+    x, y = torch.randn(kinds, vocab, generator=g), torch.randint(0, vocab, (kinds,), generator=g)
+    times = -(-rows // kinds)
+    logits, tokens = (t.to(DEV).repeat(times, *[1] * (t.dim() - 1))[:rows] for t in (x, y))
+    op = TokenLogProbs(rows, vocab, DEV, entropy=True, top=top)
+    op.run(logits, tokens)
+    want = ref.Rows(x, y, top=top)
+    ref.check(op.logp[:kinds], want.logp, want.logp_off, "logp")
+    ref.check(op.entropy[:kinds], want.entropy[:, 0], want.h_off[:, 0], "entropy")
+    a = torch.linspace(-1.0, 1.0, kinds)
+    op.backward(logits, tokens, a.to(DEV).repeat(times)[:rows], logits)
+    ref.check(logits[:kinds], *want.grad(a, None, x.dtype), "grad")
+    got = [op.logp, op.entropy, logits] + ([op.top_ids, op.top_logp] if top else [])
+    if top:
+        assert torch.equal(op.top_ids[:kinds].cpu(), want.top_ids)
+        ref.check(op.top_logp[:kinds], want.top_logp, want.top_off, "top_logp")
+    for first in range(kinds, rows, kinds):      # the same rows again
+        for t in got:
+            part = t[first:first + kinds]
+            assert torch.equal(part, t[:part.shape[0]]), first
