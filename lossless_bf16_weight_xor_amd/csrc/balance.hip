@@ -222,38 +222,43 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     };
     if (base < a.rows) fetch(row);   // while the sums are cleared
     clear();
-    uint32_t had = 0;   // turns
-    for (uint32_t at = base; at < a.rows; at += step, row += step) {   // a wave's rows
-        if constexpr (kLong) {
-            if (had == kBalanceChain) {
-                hand_over_p();
+    uint32_t at = base;
+    auto take = [&](uint32_t end) {   // a wave's rows up to there
+        for (; at < end; at += step, row += step) {
+            Turn<kF32, kVec> now = next;
+            const int64_t id = next_id;
+            if (at + step < a.rows) fetch(row + step);
+            now.hide();
+            const RowSoftmax<kF32, kVec> r(P, now.w);
+            if (r.sum != 0.0f) {   // else nothing, or nothing that counts
+                const float inv = __builtin_amdgcn_rcpf(r.sum);
 #pragma unroll
                 for (int v = 0; v < kVec; ++v)
 #pragma unroll
-                    for (int k = 0; k < kPer; ++k) p[v][k] = 0.0f;
-                had = 0;
+                    for (int k = 0; k < kPer; ++k) p[v][k] = fmaf(r.e[v][k], inv, p[v][k]);
+                const float lse = r.lse();
+                if (P.sub == 0) squares += (double)lse * lse;
+                bad_row |= !(r.sum < INFINITY);
             }
-            ++had;
+            if (!now.live) continue;
+            tokens += P.sub == 0;
+            count(id);
+            for (uint32_t j = P.sub + P.lanes; j < a.choices; j += P.lanes) count(id_at(row, j));
         }
-        Turn<kF32, kVec> now = next;
-        const int64_t id = next_id;
-        if (at + step < a.rows) fetch(row + step);
-        now.hide();
-        const RowSoftmax<kF32, kVec> r(P, now.w);
-        if (r.sum != 0.0f) {   // else nothing, or nothing that counts
-            const float inv = __builtin_amdgcn_rcpf(r.sum);
+    };
+    if constexpr (kLong) {
+        while (at < a.rows) {
+            const uint32_t turns = kBalanceChain * step;   // their rows, at most 2^24
+            take(a.rows - at > turns ? at + turns : a.rows);
+            if (at >= a.rows) break;
+            hand_over_p();
 #pragma unroll
             for (int v = 0; v < kVec; ++v)
 #pragma unroll
-                for (int k = 0; k < kPer; ++k) p[v][k] = fmaf(r.e[v][k], inv, p[v][k]);
-            const float lse = r.lse();
-            if (P.sub == 0) squares += (double)lse * lse;
-            bad_row |= !(r.sum < INFINITY);
+                for (int k = 0; k < kPer; ++k) p[v][k] = 0.0f;
         }
-        if (!now.live) continue;
-        tokens += P.sub == 0;
-        count(id);
-        for (uint32_t j = P.sub + P.lanes; j < a.choices; j += P.lanes) count(id_at(row, j));
+    } else {
+        take(a.rows);
     }
     if (tokens) atomicAdd(&s_more[kSumTokens], (unsigned long long)tokens);
     if (bad_id) s_more[kSumBadIds] = 1;

@@ -519,15 +519,15 @@ __global__ __launch_bounds__(kBlock, kTop ? 8 : 1) void logprob_kernel(LogprobAr
             for (int q = 0; q < 4; ++q) v[q] = fresh(v[q]);
         }
         add_turn<kF32, kEntropy>(mine, v, most, a.scale);
+        if constexpr (kWide) {
+            if (turn + 1 < end) load(turn + 1);
+        }
         if constexpr (kLong) {
             const uint32_t had = turn + 1 - begin;
             if (had % kLogprobChain == 0 || turn + 1 == end) {
                 s_long.add(mine, had <= kLogprobChain, a.scale);
                 if (turn + 1 == end) mine = s_long.sums();
             }
-        }
-        if constexpr (kWide) {
-            if (turn + 1 < end) load(turn + 1);
         }
     }
     Sums all = group_sums(mine, a.scale, s_tmp);
