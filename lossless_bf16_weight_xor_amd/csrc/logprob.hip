@@ -12,8 +12,8 @@
 // fp32 neither overflow nor lose their distance from the maximum.
 //
 // Forward: 2 or 4 bytes and 8 to 10 vector instructions an element.  fp32 is bound
-// by the read, at 6.2 to 6.9 TB/s (16384 x 32000: 307 us); bf16 by the read and
-// the vector units (16384 x 32000: 164 us, 6.4 TB/s; with entropy 177 us, 91 % of
+// by the read, at 6.2 to 6.9 TB/s (16384 x 32000: 305 us); bf16 by the read and
+// the vector units (16384 x 32000: 161 us, 6.5 TB/s; with entropy 177 us, 91 % of
 // the issue slots).  One fma an element instead of a difference and a product was
 // no faster: the registers it took cost as much.
 // Backward: a read and a write of every element, at 5.7 to 6.3 TB/s (4096 x 32000

@@ -31,7 +31,7 @@ inline uint32_t turns_of(uint32_t vocab, uint32_t dtype, bool aligned, uint32_t 
     return (vocab + (aligned ? 0 : vector_elems(dtype) - 1) + per - 1) / per;
 }
 // Logits of up to this many bytes are left in the last-level cache for the
-// backward pass; more are read with non-temporal loads (fp32, 16384 x 32000: 307
+// backward pass; more are read with non-temporal loads (fp32, 16384 x 32000: 305
 // us, plain 343).  Forward and backward of bf16 logits with and without: 66 MB 38.9
 // and 42.1 us, 131 MB 72.5 and 75.1; of 262 MB in fp32 131.6 and 127.3, and the
 // forward pass alone 47.8 and 42.2.
@@ -75,7 +75,7 @@ struct LogprobGradArgs {
 hipError_t launch_logprob_backward(const LogprobGradArgs &a, bool f32, hipStream_t stream);
 
 // ---- policy loss ----------------------------------------------------------------
-// A workgroup of 16 waves for each CU at most: 1e6 tokens 9.6 us, with 4 waves 28.
+// A workgroup of 16 waves for each CU at most: 1e6 tokens 10.2 us, with 4 waves 14.1.
 constexpr uint32_t kPolicyGrid = 256;
 constexpr uint32_t kPolicyThreads = 1024;
 constexpr uint32_t kPolicyAlone = 2;   // turns that one workgroup takes sooner than joining sums
@@ -171,8 +171,8 @@ __device__ __forceinline__ bool last_of(uint32_t *done, uint32_t count, uint64_t
 }
 
 // The same for all workgroups of a launch, in two levels: additions to one address
-// take some 10 to 20 ns each (1e6 tokens of the policy loss, 256 workgroups: 9.6 us, in
-// one level 11.3).  done: kDoneWords counters.
+// take some 10 to 20 ns each (1e6 tokens of the policy loss, 256 workgroups: 10.2 us, in
+// one level 11.7).  done: kDoneWords counters.
 constexpr uint32_t kDoneGroups = 16, kDoneStride = 32;   // words: a line each
 constexpr uint32_t kDoneWords = (kDoneGroups + 1) * kDoneStride;
 __device__ __forceinline__ bool last_of_launch(uint32_t *done, uint64_t dep) {

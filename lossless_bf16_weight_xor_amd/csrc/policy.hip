@@ -1,13 +1,13 @@
 // policy.hip -- the clipped policy loss over the tokens of a batch, with its
 // gradients by the log probabilities and entropies, in one launch.
 //
-// A token is 12 to 24 bytes read, 4 or 8 written and two exponentials.  All of
-// it is in 64 bits: near r = 1, where most tokens are, e^u - 1 - u and the
+// A token is 12 to 24 bytes read, 8 written (4 for a caller who leaves grad_entropy out)
+// and two exponentials.  All of it is in 64 bits: near r = 1, where most tokens are, e^u - 1 - u and the
 // distance to the clip range are differences of nearly equal numbers, and the
 // arithmetic costs next to nothing beside the launch (4096 tokens 6.3 us, with the library's
 // expm1 6.4, with its exp as well 6.5).  The clip range is compared as logarithms, logp - old
 // being exact in 64 bits.  4096 tokens take 6.4 us, of which launch and joining
-// the workgroups' sums are 5; 1e6 tokens 9.6, with reference and entropy 11.7 (2.7
+// the workgroups' sums are 5; 1e6 tokens 10.2, with reference and entropy 11.7 (2.4
 // TB/s of what they read and write).
 #include "loss.hpp"
 
